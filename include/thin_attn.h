@@ -61,7 +61,8 @@ typedef enum {
   THIN_ATTN_EUNSUPPORTED = 5   /* valid request outside what this library implements */
 } thin_attn_status;
 
-typedef enum { THIN_ATTN_FP32 = 0, THIN_ATTN_BF16 = 1 } thin_attn_dtype;
+/* FP16 and E4M3 belong to the paged operators alone. */
+typedef enum { THIN_ATTN_FP32 = 0, THIN_ATTN_BF16 = 1, THIN_ATTN_FP16 = 2, THIN_ATTN_E4M3 = 3 } thin_attn_dtype;
 
 typedef struct {
   int dtype;       /* thin_attn_dtype of q, k, v, out */
@@ -328,6 +329,143 @@ THIN_ATTN_API thin_attn_status thin_attn_halve_noalloc(int dtype, const void* K,
                                                       uint32_t round_id, void* K_out, void* V_out,
                                                       int32_t* idx_out, uint32_t* keep_bits_opt,
                                                       void* stream);
+
+/*
+ * Paged cache -- exact attention of many requests of different lengths over one pool of pages.
+ *
+ *   k_pages (n_pages, H, page, E), v_pages (n_pages, H, page, D)   any strides, last axis contiguous
+ *   table   (R, W) int32      page ids of request r in token order, rows table_row ids apart
+ *   slot    page id * page + offset: the place of one token in the pool
+ *
+ * These entry points take one argument struct each (struct_size = its sizeof), run on its device, on
+ * the caller's stream, and keep no state: no handle, no allocation, scratch only where the caller
+ * passes a workspace.  Calls that share no output and no workspace may overlap.  They can be captured
+ * into a CUDA graph; no kernel needs a value on the host.  Page ids, slots, rows and lengths are read
+ * on the device and checked there: one that points outside the pool or the table is skipped, never
+ * followed.
+ */
+
+/* Slots, block tables and the free stack of a step that gives request r n_new[r] more tokens.
+ * Requests are served in order.  status[r]:
+ *   0  placed (n_new = 0 included)
+ *   1  the free stack is short of pages for it, or was for an earlier request and it needs one too
+ *   2  its row of the table is too narrow, or lengths[r] or n_new[r] is negative
+ *   3  its tokens end behind max_tokens
+ * One that is not placed keeps its length and gets no page.  Fresh pages come off the top of the
+ * stack (free_pages[n_free - 1] first) and are written into `table`.  Token t of the step belongs to the
+ * request r with cu[r] <= t < cu[r + 1], cu the prefix sums of max(n_new, 0):
+ *   slots[t], rows[t] = r, context[t] = the tokens of r up to and with t (t's position + 1)
+ * and -1, -1, 0 for tokens of requests that were not placed and for t >= cu[R].
+ * lengths_out and n_free_out may be lengths and n_free themselves.  At most 16384 requests. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t device, R, W, page, n_pages, max_tokens, reserved;   /* n_pages: entries of free_pages */
+  const int32_t* lengths;    /* (R) */
+  const int32_t* n_new;      /* (R) */
+  int32_t* table;
+  int64_t table_row;
+  const int32_t* free_pages; /* (n_pages), the first n_free[0] of them free */
+  const int32_t* n_free;     /* (1) */
+  int32_t* lengths_out;      /* (R) */
+  int32_t* n_free_out;       /* (1) */
+  int32_t* cu;               /* (R + 1) */
+  int64_t* slots;            /* (max_tokens) */
+  int32_t* rows;             /* (max_tokens) */
+  int32_t* context;          /* (max_tokens) */
+  int32_t* status;           /* (R) */
+} thin_attn_paged_plan_args;
+THIN_ATTN_API thin_attn_status thin_attn_paged_plan(const thin_attn_paged_plan_args* a, void* stream);
+
+/* Shorten request r to keep[r] tokens (0: it has ended; negative or beyond its length: as it is) and
+ * push the pages behind them on the free stack, in order of requests; their table entries become -1. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t device, R, W, page, n_pages;
+  const int32_t* keep;       /* (R) */
+  int32_t* lengths;          /* (R), in place */
+  int32_t* table;
+  int64_t table_row;
+  int32_t* free_pages;       /* (n_pages), in place */
+  int32_t* n_free;           /* (1), in place */
+} thin_attn_paged_release_args;
+THIN_ATTN_API thin_attn_status thin_attn_paged_release(const thin_attn_paged_release_args* a, void* stream);
+
+/* Write keys and values of N tokens into their slots; a token whose slot lies outside the pool
+ * (-1 for padding) is skipped.  cache_dtype: dtype, or E4M3 with dtype BF16 or FP16: the cache then
+ * holds x / scale[h] rounded to the nearest e4m3 value, at most 448 in magnitude.
+ * With bounds: int8 (n_pages, H, 2, E) and exps int8 (n_pages, H) are brought up to date.  For the keys
+ * k that the cache holds of a page and head (a NaN counts as 0), m = max |k|: the exponent x is the least integer
+ * in [-40, 48] with 127 * 2^x >= m (48 if none), bounds row 0 = floor(min k / 2^x), row 1 =
+ * ceil(max k / 2^x), clamped to +-127.  A call that writes a page's first slot starts its bounds anew,
+ * another widens them.  The tokens of one page must be neighbours (as thin_attn_paged_plan lays
+ * them); a page met twice, with another in between, keeps sound keys but may keep the bounds of one
+ * of the two runs only.  Of two tokens with one slot, which one stays is not specified. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t device, dtype, cache_dtype, N, H, E, D, page, n_pages;
+  const void* k;             /* (N, H, E), strides in elements */
+  int64_t k_token, k_head;
+  const void* v;             /* (N, H, D) */
+  int64_t v_token, v_head;
+  const int64_t* slots;      /* (N) */
+  void* k_pages;
+  int64_t kp_page, kp_head, kp_row;
+  void* v_pages;
+  int64_t vp_page, vp_head, vp_row;
+  const float* k_scale;      /* (H), E4M3 only */
+  const float* v_scale;
+  int8_t* bounds;            /* or NULL */
+  int8_t* exps;
+} thin_attn_paged_append_args;
+THIN_ATTN_API thin_attn_status thin_attn_paged_append(const thin_attn_paged_append_args* a, void* stream);
+
+/* Attention of N query tokens.  Token n reads request rows[n] (rows NULL: request n, N <= R) and sees its
+ * first lengths[n] keys, with window > 0 the last `window` of those; query head j reads key head
+ * j / (Hq / H).  out = softmax(scale q k) v, lse = ln sum e^(scale q k).  A token that sees no key (a
+ * length of zero, pages that all lie outside the pool) gets zeros and -inf; one whose row lies
+ * outside [0, R) is padding, and its rows of out, lse and pages_out stay as they were.  A key on a page
+ * outside the pool is not seen.  Lengths are clamped to [0, W * page].
+ *
+ * top > 0 selects pages: token n and key head h attend to min(top, P) of the request's P pages: the
+ * first `first`, the last `last`, and those of the highest score (ties: the lowest index), P = the
+ * pages its lengths[n] keys reach.  A page's score is
+ *     max over the head's queries q of 2^(x + y) sum_e max(q8_e hi_e, q8_e lo_e),
+ * x, lo, hi the page's bounds (thin_attn_paged_append), q8 = q / 2^y rounded to the nearest integer,
+ * half to even, clamped to +-127 (a NaN gives 0), y from max |q| as x from max |k|.  Needs
+ * last >= 1, first >= 0, first + last <= top <= 4096, window = 0.  pages_out (N, H, top) int32:
+ * the pages' places in the request, ascending, then -1.
+ *
+ * E and D multiples of 8 (E4M3: 16) in [8, 256]; pointers and strides multiples of 16 bytes.
+ * workspace: thin_attn_paged_attention_workspace bytes, 256-byte aligned, not shared by calls that
+ * may overlap. */
+typedef struct {
+  uint32_t struct_size;
+  int32_t device, dtype, cache_dtype, N, R, W, Hq, H, E, D, page, n_pages, window, top, first, last;
+  float scale;               /* <= 0 selects 1/sqrt(E) */
+  const void* q;             /* (N, Hq, E), strides in elements */
+  int64_t q_token, q_head;
+  const void* k_pages;
+  int64_t kp_page, kp_head, kp_row;
+  const void* v_pages;
+  int64_t vp_page, vp_head, vp_row;
+  const int32_t* table;
+  int64_t table_row;
+  const int32_t* lengths;    /* (N) */
+  const int32_t* rows;       /* (N) or NULL */
+  const float* k_scale;      /* (H), E4M3 only */
+  const float* v_scale;
+  const int8_t* bounds;      /* (n_pages, H, 2, E), top > 0 only */
+  const int8_t* exps;        /* (n_pages, H) */
+  int32_t* pages_out;        /* (N, H, top) or NULL */
+  void* out;                 /* (N, Hq, D), strides in elements */
+  int64_t out_token, out_head;
+  float* lse;                /* (N, Hq) or NULL */
+  void* workspace;
+  size_t workspace_bytes;
+} thin_attn_paged_attention_args;
+THIN_ATTN_API thin_attn_status thin_attn_paged_attention_workspace(const thin_attn_paged_attention_args* a,
+                                                                   size_t* bytes);
+THIN_ATTN_API thin_attn_status thin_attn_paged_attention(const thin_attn_paged_attention_args* a, void* stream);
 
 #ifdef __cplusplus
 }

@@ -60,7 +60,9 @@ EXPORTS = ("thin_attn_version", "thin_attn_last_error", "thin_attn_create", "thi
            "thin_attn_profile_steps",
            "thin_attn_cache_create", "thin_attn_cache_destroy", "thin_attn_cache_length", "thin_attn_cache_decode",
            "thin_attn_cache_nodes", "thin_attn_cache_check", "thin_attn_sched_layout", "thin_attn_cache_decode_n",
-           "thin_attn_forward_phase", "thin_attn_nodes_layout", "thin_attn_nodes_export", "thin_attn_nodes_import")
+           "thin_attn_forward_phase", "thin_attn_nodes_layout", "thin_attn_nodes_export", "thin_attn_nodes_import",
+           "thin_attn_paged_plan", "thin_attn_paged_release", "thin_attn_paged_append",
+           "thin_attn_paged_attention_workspace", "thin_attn_paged_attention")
 
 
 def lib() -> ctypes.CDLL:
@@ -459,8 +461,13 @@ class ThinformerAttention:
                                     n_exact=self.n_exact, batch=self.batch, scale=self.scale)
 
 
+from .paged import (PagedAttentionCache, PagedPlan, paged_append, paged_attention, paged_plan,  # noqa: E402
+                    paged_release, paged_sparse_attention)
+
 __all__ = ["ThinAttention", "ThinAttentionCache", "ThinAttnError", "ThinformerAttention", "thinformer_attention",
-           "decode_trace", "exchange_batch_coresets", "lib", "LIB_PATH", "EXPORTS"]
+           "decode_trace", "exchange_batch_coresets", "lib", "LIB_PATH", "EXPORTS",
+           "PagedAttentionCache", "PagedPlan", "paged_append", "paged_attention", "paged_plan", "paged_release",
+           "paged_sparse_attention"]
 
 
 def exchange_batch_coresets(h: "ThinAttention", g: int = 2, dist=None):

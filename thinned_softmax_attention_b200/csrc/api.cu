@@ -239,20 +239,6 @@ uint32_t ctr_bh_of(const thin_attn_config& c, uint32_t bh) {
 }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (dev < 0) return;   // nothing on a device to touch
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
-
 // Wave structure of the tiles: a tile of Express batch k reads the nodes present after k
 // completed batches, whose highest level is floor(log4 k); it can run once the batch thinning
 // (k >= 1) and the merges up to that level are done.  Exact-phase tiles and batch 0 read no node.

@@ -8,6 +8,21 @@
 
 namespace thin {
 
+// Makes `dev` current for the scope of an entry point.
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = true;
+  explicit DeviceGuard(int dev) {
+    if (dev < 0) return;   // nothing on a device to touch
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+  }
+};
+
 // Halving step (c^2, pair-difference Gram, walk + gather).  dtype 0 = fp32, 1 = bf16.
 cudaError_t launch_halving_step(const StepArgs& a, int dtype, bool use_tc, cudaStream_t st);
 // Tensor-core pair-difference Gram (bf16, E and D multiples of 64); *done = false when the

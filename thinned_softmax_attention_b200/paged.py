@@ -1,0 +1,372 @@
+"""Exact attention of many requests of different lengths over one pool of cache pages.
+
+    cache = PagedAttentionCache(n_pages=4096, page=64, H=8, E=128, D=128, dtype=torch.bfloat16,
+                                max_requests=64, max_length=32768, bounds=True)
+    step = cache.plan(new_lengths, max_tokens)      # pages, slots and positions of the step's tokens
+    cache.append(k, v, step.slots)                  # (N, H, E), (N, H, D): their keys and values
+    out = cache.attend(q)                           # (R, Hq, E): one query token per request
+    out = cache.attend_sparse(q, top=64)            # the same over the 64 best pages of each request
+    cache.release(keep)                             # 0 for requests that have ended
+
+Everything stays on the device: no call waits for the GPU or reads a value back, and all of them can
+be captured into a CUDA graph.  The functions under the class take the caller's own tensors.  A page
+holds ``page`` tokens of every key head, k_pages (n_pages, H, page, E) and v_pages (n_pages, H, page,
+D), in any strides with a contiguous last axis; query head j reads key head j // (Hq // H).
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from functools import lru_cache
+from typing import NamedTuple, Optional, Tuple
+
+import torch
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3}
+# the argument structs of include/thin_attn.h, field by field
+_PLAN = struct.Struct("@I7iPPPqPPPPPPPPP")
+_RELEASE = struct.Struct("@I5iPPPqPP")
+_APPEND = struct.Struct("@I9iPqqPqqPPqqqPqqqPPPP")
+_ATTENTION = struct.Struct("@I16ifPqqPqqqPqqqPqPPPPPPPPqqPPN")
+
+_fns = None
+
+
+def _functions():
+    global _fns
+    if _fns is None:
+        from . import lib
+        L = lib()
+        L.thin_attn_paged_attention_workspace.argtypes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)]
+        for f in ("plan", "release", "append", "attention"):
+            getattr(L, f"thin_attn_paged_{f}").argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+        _fns = L
+    return _fns
+
+
+def _raise(status: int):
+    from . import _check
+    _check(status)
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    _need(t.is_cuda, f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return t.device
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: torch.device):
+    if t.dtype != dtype or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} ({n},) on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _table(t: torch.Tensor, device: torch.device):
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"table: expected int32 (R, W) with contiguous rows on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: torch.device):
+    """(n_pages, H, page, E, D) of the pool."""
+    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
+        raise ValueError(f"k_pages (n_pages, H, page, E) and v_pages (n_pages, H, page, D): got {tuple(k_pages.shape)} and {tuple(v_pages.shape)}")
+    if k_pages.dtype != v_pages.dtype or k_pages.device != device or v_pages.device != device:
+        raise ValueError(f"k_pages and v_pages: expected one type on {device}, got {k_pages.dtype} on {k_pages.device} and {v_pages.dtype} on {v_pages.device}")
+    if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+        raise ValueError("k_pages and v_pages: the last axis must be contiguous")
+    return (*k_pages.shape, v_pages.shape[3])
+
+
+def _types(dtype: torch.dtype, cache: torch.dtype) -> Tuple[int, int]:
+    if dtype not in _DTYPES or dtype == torch.float8_e4m3fn:
+        raise ValueError(f"dtype {dtype}: expected float32, bfloat16 or float16")
+    if cache != dtype and (cache != torch.float8_e4m3fn or dtype == torch.float32):
+        raise ValueError(f"pages of {cache} with {dtype}: expected {dtype}, or float8_e4m3fn with bfloat16 or float16")
+    return _DTYPES[dtype], _DTYPES[cache]
+
+
+def _scales(k_scale, v_scale, cache: torch.dtype, H: int, device: torch.device) -> Tuple[int, int]:
+    if cache != torch.float8_e4m3fn:
+        _need(k_scale is None and v_scale is None, "k_scale and v_scale belong to float8_e4m3fn pages")
+        return 0, 0
+    _need(k_scale is not None and v_scale is not None, "float8_e4m3fn pages need k_scale and v_scale")
+    _vector(k_scale, "k_scale", H, torch.float32, device)
+    _vector(v_scale, "v_scale", H, torch.float32, device)
+    return k_scale.data_ptr(), v_scale.data_ptr()
+
+
+def _bounds(bounds, n_pages: int, H: int, E: int, device: torch.device) -> Tuple[int, int]:
+    lohi, exps = bounds
+    if lohi.dtype != torch.int8 or lohi.device != device or lohi.shape != (n_pages, H, 2, E) or not lohi.is_contiguous():
+        raise ValueError(f"bounds[0]: expected contiguous int8 {(n_pages, H, 2, E)} on {device}")
+    if exps.dtype != torch.int8 or exps.device != device or exps.shape != (n_pages, H) or not exps.is_contiguous():
+        raise ValueError(f"bounds[1]: expected contiguous int8 {(n_pages, H)} on {device}")
+    return lohi.data_ptr(), exps.data_ptr()
+
+
+class PagedPlan(NamedTuple):
+    """A step's places.  ``lengths`` (R) and ``n_free`` (1) after the step; ``cu`` (R + 1) the prefix
+    sums of the new lengths; per token of the step ``slots`` int64, ``rows`` (its request) and
+    ``context`` (the keys it sees, itself among them), -1, -1 and 0 where there is none; ``status``
+    (R): 0 placed, 1 out of pages, 2 table row too narrow or a negative length, 3 behind max_tokens."""
+    lengths: torch.Tensor
+    n_free: torch.Tensor
+    cu: torch.Tensor
+    slots: torch.Tensor
+    rows: torch.Tensor
+    context: torch.Tensor
+    status: torch.Tensor
+
+
+def paged_plan(lengths: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: torch.Tensor, n_free: torch.Tensor,
+               page: int, max_tokens: int, inplace: bool = False) -> PagedPlan:
+    """Block tables and slots of a step that gives request r ``new[r]`` more tokens, on the device.
+
+    lengths, new (R) int32; table (R, W) int32, whose fresh entries are written; free int32, its
+    first ``n_free[0]`` entries the free pages (the last one is taken first).  Requests are served
+    in order; one that finds no room keeps its length and gets nothing (``status``).  The step's
+    tokens are laid out request by request, ``max_tokens`` places in all.  ``lengths`` and
+    ``n_free`` themselves change only with ``inplace=True``."""
+    dev = _device(lengths, "lengths")
+    R = lengths.shape[0]
+    _vector(lengths, "lengths", R, torch.int32, dev)
+    _vector(new, "new", R, torch.int32, dev)
+    _table(table, dev)
+    _need(table.shape[0] == R, f"table: {table.shape[0]} rows for {R} requests")
+    _vector(free, "free", free.numel(), torch.int32, dev)
+    _vector(n_free, "n_free", 1, torch.int32, dev)
+    _need(max_tokens >= 0 and page >= 1, f"page={page} and max_tokens={max_tokens}: expected page >= 1, max_tokens >= 0")
+    # one allocation: slots first (8 bytes each), then the 4-byte arrays
+    T = max_tokens
+    n32 = 2 * T + 2 * R + 1 + (0 if inplace else R + 1)
+    buf = torch.empty(2 * T + n32, dtype=torch.int32, device=dev)
+    slots = buf[:2 * T].view(torch.int64)
+    parts = buf[2 * T:].split([T, T, R + 1, R] + ([] if inplace else [R, 1]))
+    rows, context, cu, status = parts[:4]
+    lengths_out, n_free_out = (lengths, n_free) if inplace else parts[4:]
+    p = _PLAN.pack(_PLAN.size, dev.index, R, table.shape[1], page, free.numel(), T, 0, lengths.data_ptr(), new.data_ptr(),
+                   table.data_ptr(), table.stride(0), free.data_ptr(), n_free.data_ptr(), lengths_out.data_ptr(),
+                   n_free_out.data_ptr(), cu.data_ptr(), slots.data_ptr(), rows.data_ptr(), context.data_ptr(),
+                   status.data_ptr())
+    s = _functions().thin_attn_paged_plan(p, _stream(dev))
+    if s:
+        _raise(s)
+    return PagedPlan(lengths_out, n_free_out, cu, slots, rows, context, status)
+
+
+def paged_release(keep: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor, free: torch.Tensor,
+                  n_free: torch.Tensor, page: int) -> None:
+    """Shorten request r to ``keep[r]`` tokens (0: it has ended; negative: as it is) and give the pages
+    behind them back; lengths, table, free and n_free change in place."""
+    dev = _device(lengths, "lengths")
+    R = lengths.shape[0]
+    _vector(lengths, "lengths", R, torch.int32, dev)
+    _vector(keep, "keep", R, torch.int32, dev)
+    _table(table, dev)
+    _need(table.shape[0] == R, f"table: {table.shape[0]} rows for {R} requests")
+    _vector(free, "free", free.numel(), torch.int32, dev)
+    _vector(n_free, "n_free", 1, torch.int32, dev)
+    p = _RELEASE.pack(_RELEASE.size, dev.index, R, table.shape[1], page, free.numel(), keep.data_ptr(), lengths.data_ptr(),
+                      table.data_ptr(), table.stride(0), free.data_ptr(), n_free.data_ptr())
+    s = _functions().thin_attn_paged_release(p, _stream(dev))
+    if s:
+        _raise(s)
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, *,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 bounds: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> None:
+    """Write k (N, H, E) and v (N, H, D) into their slots; a slot outside the pool (-1) is skipped.
+
+    float8_e4m3fn pages hold x / scale[h], rounded to the nearest value, at most 448 in magnitude.
+    ``bounds`` = (int8 (n_pages, H, 2, E), int8 (n_pages, H)): the pages' key bounds for
+    ``paged_sparse_attention``, widened by the new keys, or started anew where a page's first slot
+    is written; the tokens of one page must then be neighbours, as ``paged_plan`` lays them."""
+    dev = _device(k, "k")
+    P, H, page, E, D = _pool(k_pages, v_pages, dev)
+    N = k.shape[0]
+    if k.shape != (N, H, E) or v.shape != (N, H, D) or k.dtype != v.dtype or v.device != dev:
+        raise ValueError(f"k and v: expected {(N, H, E)} and {(N, H, D)} of one type on {dev}, got {k.dtype} {tuple(k.shape)} "
+                         f"and {v.dtype} {tuple(v.shape)} on {v.device}")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v: the last axis must be contiguous")
+    _vector(slots, "slots", N, torch.int64, dev)
+    dt, ct = _types(k.dtype, k_pages.dtype)
+    ks, vs = _scales(k_scale, v_scale, k_pages.dtype, H, dev)
+    b, x = (0, 0) if bounds is None else _bounds(bounds, P, H, E, dev)
+    p = _APPEND.pack(_APPEND.size, dev.index, dt, ct, N, H, E, D, page, P, k.data_ptr(), *k.stride()[:2], v.data_ptr(),
+                     *v.stride()[:2], slots.data_ptr(), k_pages.data_ptr(), *k_pages.stride()[:3], v_pages.data_ptr(),
+                     *v_pages.stride()[:3], ks, vs, b, x)
+    s = _functions().thin_attn_paged_append(p, _stream(dev))
+    if s:
+        _raise(s)
+
+
+@lru_cache(maxsize=1024)
+def _workspace_bytes(dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last, has_rows) -> int:
+    p = _ATTENTION.pack(_ATTENTION.size, 0, dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last, 0.0,
+                        *[0] * 14, int(has_rows), *[0] * 11)   # of the pointers only whether there are rows counts
+    n = ctypes.c_size_t()
+    _raise(_functions().thin_attn_paged_attention_workspace(p, ctypes.byref(n)))
+    return n.value
+
+
+def _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, window, bounds, top, first, last, out,
+               lse, pages):
+    dev = _device(q, "q")
+    P, H, page, E, D = _pool(k_pages, v_pages, dev)
+    if q.dim() != 3 or q.shape[2] != E or q.stride(2) != 1:
+        raise ValueError(f"q: expected (N, Hq, {E}) with a contiguous last axis, got {tuple(q.shape)}")
+    N, Hq, _ = q.shape
+    _need(Hq % H == 0 and Hq >= H, f"{Hq} query heads over {H} key heads")
+    _table(table, dev)
+    R, W = table.shape
+    _vector(lengths, "lengths", N, torch.int32, dev)
+    if rows is not None:
+        _vector(rows, "rows", N, torch.int32, dev)
+    dt, ct = _types(q.dtype, k_pages.dtype)
+    ks, vs = _scales(k_scale, v_scale, k_pages.dtype, H, dev)
+    if out is None:
+        # rows of padding tokens are not written: zeros there when the buffer is made here
+        out = (torch.empty if rows is None else torch.zeros)((N, Hq, D), dtype=q.dtype, device=dev)
+    elif out.shape != (N, Hq, D) or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1:
+        raise ValueError(f"out: expected {q.dtype} {(N, Hq, D)} with a contiguous last axis on {dev}")
+    if lse is not None and (lse.shape != (N, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev):
+        raise ValueError(f"lse: expected contiguous float32 {(N, Hq)} on {dev}, got {lse.dtype} {tuple(lse.shape)}")
+    b, x = (0, 0) if bounds is None else _bounds(bounds, P, H, E, dev)
+    n = _workspace_bytes(dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last, rows is not None)
+    # scratch of this call alone: the caching allocator hands it on in stream order, and a capture
+    # gets its own from the graph's pool
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    p = _ATTENTION.pack(_ATTENTION.size, dev.index, dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last,
+                        0.0 if scale is None else scale, q.data_ptr(), q.stride(0), q.stride(1), k_pages.data_ptr(),
+                        *k_pages.stride()[:3], v_pages.data_ptr(), *v_pages.stride()[:3], table.data_ptr(), table.stride(0),
+                        lengths.data_ptr(), 0 if rows is None else rows.data_ptr(), ks, vs, b, x,
+                        0 if pages is None else pages.data_ptr(), out.data_ptr(), out.stride(0), out.stride(1),
+                        0 if lse is None else lse.data_ptr(), 0 if ws is None else ws.data_ptr(), n)
+    s = _functions().thin_attn_paged_attention(p, _stream(dev))
+    if s:
+        _raise(s)
+    return out
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                    lengths: torch.Tensor, *, rows: Optional[torch.Tensor] = None, window: int = 0,
+                    scale: Optional[float] = None, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, return_lse: bool = False):
+    """Attention of query tokens q (N, Hq, E) over the paged cache: out (N, Hq, D), or (out, lse) with
+    ``return_lse=True`` (lse (N, Hq) fp32, implied by a given ``lse``).
+
+    Token n belongs to request ``rows[n]`` (without ``rows``: request n) and sees its first
+    ``lengths[n]`` keys, with ``window`` the last ``window`` of those.  Several tokens of a request
+    are several rows of q with lengths that grow by one (``paged_plan``'s ``rows`` and ``context``).  One that sees
+    nothing gets zeros and -inf; one whose row is negative is padding and leaves its rows of
+    ``out`` and ``lse`` as they were (zeros in buffers made here).
+    The keys are read once per query token: made for decode and short drafts, not for long prompts."""
+    if lse is None and return_lse:
+        lse = _new_lse(q, rows)
+    out = _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, window, None, 0, 0, 0, out, lse, None)
+    return out if lse is None else (out, lse)
+
+
+def _new_lse(q: torch.Tensor, rows) -> torch.Tensor:
+    _device(q, "q")
+    return (torch.empty if rows is None else torch.zeros)(q.shape[:2], dtype=torch.float32, device=q.device)
+
+
+def paged_sparse_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                           lengths: torch.Tensor, bounds: Tuple[torch.Tensor, torch.Tensor], top: int, *, first: int = 1,
+                           last: int = 1, rows: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                           k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           return_lse: bool = False, return_pages: bool = False):
+    """``paged_attention`` over at most ``top`` pages per token and key head: the request's first
+    ``first`` and last ``last`` ones, and those whose ``bounds`` (``paged_append``) promise the largest
+    q . k to any of the head's queries.  Returns out, then lse and pages as asked; pages (N, H, top)
+    int32 holds the chosen pages' places in the request in ascending order, then -1."""
+    if lse is None and return_lse:
+        lse = _new_lse(q, rows)
+    _need(top >= 1, f"top={top}: expected at least one page")
+    pages = None
+    if return_pages:
+        pages = torch.empty((q.shape[0], k_pages.shape[1], top), dtype=torch.int32, device=q.device)
+        if rows is not None:
+            pages.fill_(-1)
+    out = _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, 0, bounds, top, first, last, out,
+                     lse, pages)
+    got = (out,) + ((lse,) if lse is not None else ()) + ((pages,) if return_pages else ())
+    return got if len(got) > 1 else out
+
+
+class PagedAttentionCache:
+    """A pool of cache pages and the block tables of up to ``max_requests`` requests.
+
+    ``plan``, ``append``, ``attend``, ``attend_sparse`` and ``release`` are the module's functions over the cache's
+    own tensors: ``k_pages``, ``v_pages``, ``table``, ``lengths``, ``free``, ``n_free`` and, with ``bounds=True``,
+    ``bounds``.  They are updated in place, so a captured step replays on the cache as it then
+    stands.  ``cache_dtype=torch.float8_e4m3fn`` halves the pool; ``k_scale`` and ``v_scale`` (H) fp32 are
+    then required.  One cache's calls share these tensors: issue them on one stream, or order the
+    streams."""
+
+    def __init__(self, n_pages: int, page: int, H: int, E: int, D: int, dtype: torch.dtype, max_requests: int,
+                 max_length: int, *, cache_dtype: Optional[torch.dtype] = None, bounds: bool = False,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, device: int = 0):
+        dev = torch.device("cuda", device)
+        ct = cache_dtype or dtype
+        _need(min(n_pages, page, H, E, D, max_requests, max_length) >= 1,
+              f"n_pages={n_pages} page={page} H={H} E={E} D={D} max_requests={max_requests} max_length={max_length}: all >= 1")
+        _types(dtype, ct)
+        _scales(k_scale, v_scale, ct, H, dev)
+        self.dtype, self.device, self.page, self.scale = dtype, dev, page, scale
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.k_pages = torch.zeros((n_pages, H, page, E), dtype=ct, device=dev)
+        self.v_pages = torch.zeros((n_pages, H, page, D), dtype=ct, device=dev)
+        self.bounds = None
+        if bounds:
+            self.bounds = (torch.zeros((n_pages, H, 2, E), dtype=torch.int8, device=dev),
+                           torch.zeros((n_pages, H), dtype=torch.int8, device=dev))
+        self.table = torch.full((max_requests, -(-max_length // page)), -1, dtype=torch.int32, device=dev)
+        self.lengths = torch.zeros(max_requests, dtype=torch.int32, device=dev)
+        self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=dev)
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=dev)
+
+    def plan(self, new: torch.Tensor, max_tokens: int) -> PagedPlan:
+        return paged_plan(self.lengths, new, self.table, self.free, self.n_free, self.page, max_tokens, inplace=True)
+
+    def release(self, keep: torch.Tensor) -> None:
+        paged_release(keep, self.lengths, self.table, self.free, self.n_free, self.page)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+        paged_append(k, v, slots, self.k_pages, self.v_pages, k_scale=self.k_scale, v_scale=self.v_scale, bounds=self.bounds)
+
+    def attend(self, q: torch.Tensor, *, rows: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+               window: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               return_lse: bool = False):
+        """q (max_requests, Hq, E), one token per request that sees all of its keys; or with ``rows``
+        and ``lengths`` (``plan``'s ``rows`` and ``context``) any tokens."""
+        return paged_attention(q, self.k_pages, self.v_pages, self.table, self._seen(rows, lengths), rows=rows, window=window,
+                               scale=self.scale, k_scale=self.k_scale, v_scale=self.v_scale, out=out, lse=lse,
+                               return_lse=return_lse)
+
+    def attend_sparse(self, q: torch.Tensor, top: int, *, first: int = 1, last: int = 1,
+                      rows: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                      return_pages: bool = False):
+        _need(self.bounds is not None, "attend_sparse needs a cache made with bounds=True")
+        return paged_sparse_attention(q, self.k_pages, self.v_pages, self.table, self._seen(rows, lengths), self.bounds, top,
+                                      first=first, last=last, rows=rows, scale=self.scale, k_scale=self.k_scale,
+                                      v_scale=self.v_scale, out=out, lse=lse, return_lse=return_lse,
+                                      return_pages=return_pages)
+
+    def _seen(self, rows, lengths):
+        _need(rows is None or lengths is not None, "rows need lengths: the keys that each token sees")
+        return self.lengths if lengths is None else lengths
