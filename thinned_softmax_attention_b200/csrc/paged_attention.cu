@@ -1,7 +1,32 @@
-// Attention of single query tokens over lists of cache pages.
+// Attention of single query tokens over lists of cache pages, split over the keys and joined.
 //
-// A CTA per (token, query head); its warps take every fourth key, each with a running maximum and sum
-// (m <- max(m, z), the sums so far times 2^(m_old - m)), and are joined at the end.
+//   z_j = s q.k_j log2 e,  m = max z,  l = sum 2^(z_j - m),  o = sum 2^(z_j - m) v_j / l
+// A key head's G query rows share its keys, so each key and value row is read once and used for G dot
+// products: about 2 G FLOP per byte, far below the machine's balance.  HBM bounds it; everything below
+// serves to keep enough reads in flight and the tail short.
+//
+// Work.  The keys of (token, key head) pairs, token by token, form one line of units of
+// 16 keys per warp.  Every CTA of a fixed grid takes an equal stretch of that line, whatever the
+// lengths are (they are only known on the device): long requests are split, short ones
+// packed.  A pair that lies in one CTA is finished there; one that is cut leaves a partial (m, l, o)
+// per CTA, and the join kernel, launched behind it, adds up those of each cut pair.
+//
+// Reads.  A warp owns a ring of stages in shared memory, 16 keys and values each, filled by its own
+// asynchronous copies (no barrier of the CTA in the loop): the ring runs on across pairs, so the next
+// pair's keys arrive while this one is joined.  The page ids are fetched a step ahead.  Rows that
+// are not seen (behind the length, before the window, on a page outside the pool) are filled with zeros, so that
+// nothing stored there, NaN or not, meets a weight of zero.
+//
+// Products (16-bit and 8-bit caches), mma m16n8k16: S = Q K^T with the rows of Q as M, O += P V.  The
+// order of the summed index is free, so a lane takes its B fragments of K as whole 16-byte pieces of
+// a row, and the column order of S is chosen so that S's accumulator is P's A fragment as it stands:
+// lane (r, c) holds the columns of keys 4 c .. 4 c + 3, reads those four rows of V as 16-byte pieces
+// (of d = DC (r + 8 i) ..) and pairs them up with byte permutations.  No transposing load, no shuffle but
+// the row maximum.  G <= 8 leaves the tile's upper 8 rows free: they carry P's rounding error, so P
+// keeps 16 bits and more at no cost; G <= 16 issues that product separately (16-bit caches).
+// fp32 caches run on CUDA cores in fp32.
+#include <type_traits>
+
 #include "paged.h"
 #include "paged_types.cuh"
 
@@ -9,86 +34,841 @@ namespace thin {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kKeys = 16;          // keys of a warp's stage
+constexpr int kMaxCtas = 296;      // 148 SMs x 2
 
-template <typename T, typename C>
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(PagedAttn p) {
-  const thin_attn_paged_attention_args& a = p.a;
-  const int n = blockIdx.x, qh = blockIdx.y, h = qh / (a.Hq / a.H);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = a.rows ? a.rows[n] : n;
-  if (row < 0 || row >= a.R) return;   // padding: its outputs stay as they were
-  const int32_t* ids = p.ids + (p.list_rows ? row : n) * p.ids_token + h * p.ids_head;
-  const int len = min(max(p.keys[n], 0), p.list_width * a.page);
-  const float sk = p.scale_log2e * (a.k_scale ? a.k_scale[h] : 1.f), sv = a.v_scale ? a.v_scale[h] : 1.f;
-  float q[8], o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = o[i] = 0.f;
-  if (lane * 8 < a.E) load8((const T*)a.q + n * a.q_token + qh * a.q_head + lane * 8, q);
-  float m = -INFINITY, l = 0.f;
-  for (int j = (a.window && len > a.window ? len - a.window : 0) + warp; j < len; j += kWarps) {
-    const int id = ids[j / a.page], off = j % a.page;
-    if (id < 0 || id >= a.n_pages) continue;
-    float z = 0.f, v[8];
-    if (lane * 8 < a.E) {
-      float k[8];
-      load8((const C*)a.k_pages + id * a.kp_page + h * a.kp_head + off * a.kp_row + lane * 8, k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z = fmaf(q[i], k[i], z);
-    }
-    if (lane * 8 < a.D) load8((const C*)a.v_pages + id * a.vp_page + h * a.vp_head + off * a.vp_row + lane * 8, v);
-#pragma unroll
-    for (int s = 16; s; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    z *= sk;
-    const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : exp2f(m - mn), w = z == -INFINITY ? 0.f : exp2f(z - mn);
-    m = mn;
-    l = l * f + w;
-    if (lane * 8 < a.D) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(w, v[i], o[i] * f);
-    }
-  }
-  __shared__ float m_s[kWarps], l_s[kWarps], o_s[kWarps][256];
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
-  }
-  if (lane * 8 < a.D) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o_s[warp][lane * 8 + i] = o[i];
-  }
-  __syncthreads();
-  float M = -INFINITY, L = 0.f, f[kWarps];
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m_s[w]);
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = m_s[w] == -INFINITY ? 0.f : exp2f(m_s[w] - M);
-    L += l_s[w] * f[w];
-  }
-  const float inv = L == 0.f ? 0.f : sv / L;
-  for (int d = threadIdx.x; d < a.D; d += kWarps * 32) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += o_s[w][d] * f[w];
-    ((T*)a.out)[n * a.out_token + qh * a.out_head + d] = elem_of<T>(x * inv);
-  }
-  if (threadIdx.x == 0 && a.lse)
-    a.lse[(int64_t)n * a.Hq + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+// One token of the call: its row of outputs, its visible keys [start, len) and their units.
+struct Token {
+  int len, start, units;
+  const int32_t* ids;
+  bool live;   // not padding
+};
+
+template <int UNIT>
+__device__ __forceinline__ Token token_of(const PagedAttn& p, int n) {
+  Token t;
+  const int row = p.a.rows ? p.a.rows[n] : n;
+  t.live = row >= 0 && row < p.a.R;
+  t.len = t.live ? min(max(p.keys[n], 0), p.list_width * p.a.page) : 0;
+  t.start = p.a.window && t.len > p.a.window ? t.len - p.a.window : 0;
+  const int first = t.start & ~(kKeys - 1);
+  t.units = (t.len - first + UNIT - 1) / UNIT;
+  t.ids = p.ids + (p.list_rows ? row : n) * p.ids_token;
+  return t;
 }
 
-template <typename T, typename C>
-cudaError_t launch_t(const PagedAttn& p, cudaStream_t st) {
-  attention_kernel<T, C><<<dim3(p.a.N, p.a.Hq), kWarps * 32, 0, st>>>(p);
-  return cudaGetLastError();
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
+  const int n = full ? 16 : 0;   // the rest is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows of a stage lie one behind the other; the 16-byte pieces of a row are permuted within groups of
+// eight so that the fragment reads below meet every bank once: K's quarter-warps read the same pieces of two
+// neighbouring rows, V's two neighbouring pieces of rows 4 apart.
+__device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) ^ (((row >> 2) & 3) << 1); }
+
+template <typename M>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  if constexpr (std::is_same<M, __nv_bfloat16>::value)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <typename M>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (std::is_same<M, __nv_bfloat16>::value)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else
+    return __half22float2(*(const __half2*)&w);
+}
+template <typename M>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<M, __nv_bfloat16>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 values as two fp16 ones (exact).
+__device__ __forceinline__ uint32_t widen2(uint32_t b) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)b, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+// ---------------------------------------------------------------------------------------------
+// One warp's part of a tile of ROWS query rows, on the tensor cores.
+// ---------------------------------------------------------------------------------------------
+template <typename T, typename C, int HD, int ROWS_>
+struct MmaTile {
+  static constexpr int ROWS = ROWS_;
+  static constexpr int kSmem = 0;
+  static constexpr bool k8 = sizeof(C) == 1;
+  using M = typename std::conditional<k8, __half, T>::type;   // the products' type
+  static constexpr int RB = HD * (int)sizeof(C);              // bytes of a stage's row
+  static constexpr int DC = 16 / (int)sizeof(C);              // elements of a 16-byte piece
+  static constexpr int KJ = RB / 64, VI = RB / 128;           // pieces of K and V per lane and row
+  static constexpr int QW = DC / 2;                           // words of Q per piece
+  static constexpr bool kSplit = !k8 || ROWS == 8;            // P as two numbers
+  static_assert(ROWS == 8 || ROWS == 16, "");
+  static_assert(VI >= 1 && KJ == 2 * VI, "");
+
+  uint32_t q[KJ][ROWS / 8][QW];
+  float o[VI][DC][4];
+  float m[2], l[2], sc[2];
+
+  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float*) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int x = 0; x < ROWS / 8; ++x) {
+      const int g = r + 8 * x;
+      const T* src = (const T*)p.a.q + n * p.a.q_token + (row0 + g) * p.a.q_head;
+      uint32_t w[KJ][QW];
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        const int e = (c + 4 * j) * DC;
+#pragma unroll
+        for (int y = 0; y < QW / 4; ++y) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (g < rows && e < p.a.E) u = ((const uint4*)(src + e))[y];
+          w[j][4 * y] = u.x;
+          w[j][4 * y + 1] = u.y;
+          w[j][4 * y + 2] = u.z;
+          w[j][4 * y + 3] = u.w;
+        }
+      }
+      sc[x] = scale;
+      if constexpr (k8 && !std::is_same<T, __half>::value) {
+        // q into fp16, times the power of two that brings the row's largest value to 2^13 .. 2^14: what
+        // is below 2^-38 of that loses bits
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+          for (int y = 0; y < QW; ++y) {
+            const float2 f = unpack2<T>(w[j][y]);
+            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int up = min(max(140 - (int)(__float_as_uint(mx) >> 23), -100), 100);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+          for (int y = 0; y < QW; ++y) {
+            const float2 f = unpack2<T>(w[j][y]);
+            w[j][y] = pack2<__half>(f.x * pow2f(up), f.y * pow2f(up));
+          }
+        sc[x] = scale * pow2f(-up);
+      }
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+#pragma unroll
+        for (int y = 0; y < QW; ++y) q[j][x][y] = w[j][y];
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < VI; ++i)
+#pragma unroll
+      for (int y = 0; y < DC; ++y) o[i][y][0] = o[i][y][1] = o[i][y][2] = o[i][y][3] = 0.f;
+  }
+
+  // One stage: keys at smem address ks, values at vs; bit j of `seen` is key j's.
+  __device__ __forceinline__ void step(const PagedAttn& p, uint32_t ks, uint32_t vs, uint32_t seen, int lane, float*) {
+    const int r = lane >> 2, c = lane & 3;
+    float s[2][4] = {};
+    const uint32_t zero = 0;
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+      if (j * 4 * DC >= p.a.E) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int row = 4 * (r >> 1) + 2 * t + (r & 1);   // column r of S's tile t
+        const uint4 u = lds16(ks + row * RB + (((c + 4 * j) ^ swizzle(row)) << 4));
+        uint32_t b[QW];
+        if constexpr (k8) {
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            b[2 * y] = widen2(w[y] & 0xFFFF);
+            b[2 * y + 1] = widen2(w[y] >> 16);
+          }
+        } else {
+          b[0] = u.x;
+          b[1] = u.y;
+          b[2] = u.z;
+          b[3] = u.w;
+        }
+#pragma unroll
+        for (int y = 0; y < QW; y += 2) {
+          const uint32_t a[4] = {q[j][0][y], ROWS == 16 ? q[j][ROWS / 8 - 1][y] : zero, q[j][0][y + 1],
+                                 ROWS == 16 ? q[j][ROWS / 8 - 1][y + 1] : zero};
+          mma<M>(s[t], a, b[y], b[y + 1]);
+        }
+      }
+    }
+    // s[t][2 x + u] = row r + 8 x against key 4 c + 2 t + u
+    // z is rounded before the maximum is taken, so that z - m is 0 at the maximum, however large both are
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int x = 0; x < ROWS / 8; ++x) {
+        s[t][2 * x] *= sc[x];
+        s[t][2 * x + 1] *= sc[x];
+      }
+    if (seen != 0xFFFF) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (!((seen >> (4 * c + 2 * t + u)) & 1)) s[t][u] = s[t][2 + u] = -INFINITY;
+    }
+    uint32_t hi[2][2], lo[2][2];   // [x][t]
+    float f[2];
+    bool grown = false;
+#pragma unroll
+    for (int x = 0; x < ROWS / 8; ++x) {
+      float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[x], mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      f[x] = ex2(m[x] - ref);
+      grown |= mn != m[x];
+      m[x] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float a = ex2(s[t][2 * x] - ref), b = ex2(s[t][2 * x + 1] - ref);
+        sum += a + b;
+        hi[x][t] = pack2<M>(a, b);
+        if constexpr (kSplit) {
+          const float2 h = unpack2<M>(hi[x][t]);
+          lo[x][t] = pack2<M>(a - h.x, b - h.y);
+        }
+      }
+      l[x] = l[x] * f[x] + sum;
+    }
+    if (__any_sync(0xffffffffu, grown)) {
+      const float f1 = ROWS == 16 ? f[ROWS / 8 - 1] : f[0];
+#pragma unroll
+      for (int i = 0; i < VI; ++i)
+#pragma unroll
+        for (int y = 0; y < DC; ++y) {
+          o[i][y][0] *= f[0];
+          o[i][y][1] *= f[0];
+          o[i][y][2] *= f1;
+          o[i][y][3] *= f1;
+        }
+    }
+    uint32_t a[4] = {hi[0][0], ROWS == 16 ? hi[ROWS / 8 - 1][0] : lo[0][0], hi[0][1], ROWS == 16 ? hi[ROWS / 8 - 1][1] : lo[0][1]};
+    uint32_t a2[4] = {lo[0][0], lo[ROWS / 8 - 1][0], lo[0][1], lo[ROWS / 8 - 1][1]};
+#pragma unroll
+    for (int i = 0; i < VI; ++i) {
+      if (i * 8 * DC >= p.a.D) break;
+      uint32_t v[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 4 * c + k;
+        const uint4 u = lds16(vs + row * RB + (((r + 8 * i) ^ swizzle(row)) << 4));
+        v[k][0] = u.x;
+        v[k][1] = u.y;
+        v[k][2] = u.z;
+        v[k][3] = u.w;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (k8) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            // bytes 2 y and 2 y + 1 of the word, those of two keys side by side
+            const uint32_t b0 = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+            const uint32_t b1 = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t p0 = widen2(z ? b0 >> 16 : b0 & 0xFFFF), p1 = widen2(z ? b1 >> 16 : b1 & 0xFFFF);
+              mma<M>(o[i][4 * w + 2 * y + z], a, p0, p1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t sel = y ? 0x7632 : 0x5410;
+            const uint32_t b0 = __byte_perm(v[0][w], v[1][w], sel), b1 = __byte_perm(v[2][w], v[3][w], sel);
+            mma<M>(o[i][2 * w + y], a, b0, b1);
+            if constexpr (kSplit && ROWS == 16) mma<M>(o[i][2 * w + y], a2, b0, b1);
+          }
+        }
+      }
+    }
+  }
+
+  // The sums over the lanes of a row; then (m, l) of row g at ml[2 g].
+  __device__ __forceinline__ void finish(float* ml, int lane) {
+#pragma unroll
+    for (int x = 0; x < ROWS / 8; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      if ((lane & 3) == 0) {
+        ml[2 * ((lane >> 2) + 8 * x)] = m[x];
+        ml[2 * ((lane >> 2) + 8 * x) + 1] = l[x];
+      }
+    }
+  }
+  // Columns [64 part, 64 part + 64) of o into dst (ROWS x 68).
+  __device__ __forceinline__ void put(float* dst, int part, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < VI; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int d = DC * (2 * c + u + 8 * i);
+#pragma unroll
+        for (int y = 0; y < DC; y += 4) {
+          if ((d + y) / 64 != part) continue;
+          if constexpr (ROWS == 8) {
+            float4 x = make_float4(o[i][y][u] + o[i][y][2 + u], o[i][y + 1][u] + o[i][y + 1][2 + u],
+                                   o[i][y + 2][u] + o[i][y + 2][2 + u], o[i][y + 3][u] + o[i][y + 3][2 + u]);
+            *(float4*)(dst + r * 68 + (d + y) % 64) = x;
+          } else {
+            *(float4*)(dst + r * 68 + (d + y) % 64) = make_float4(o[i][y][u], o[i][y + 1][u], o[i][y + 2][u], o[i][y + 3][u]);
+            *(float4*)(dst + (r + 8) * 68 + (d + y) % 64) =
+                make_float4(o[i][y][2 + u], o[i][y + 1][2 + u], o[i][y + 2][2 + u], o[i][y + 3][2 + u]);
+          }
+        }
+      }
+  }
+};
+
+// ---------------------------------------------------------------------------------------------
+// The same in fp32 on CUDA cores: a lane pair per key for the scores, a lane per four columns for o.
+// ---------------------------------------------------------------------------------------------
+template <int HD>
+struct SimtTile {
+  static constexpr int ROWS = 8;
+  static constexpr int RB = HD * 4;
+  static constexpr int CB = HD > 128 ? HD / 128 : 1;          // float4 columns per lane
+  static constexpr int kSmem = (ROWS * HD + ROWS * kKeys) * 4;   // q and p of a warp
+
+  float o[ROWS][CB][4];
+  float m[ROWS], l[ROWS], sc;
+  int rows;
+
+  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows_, float scale, int lane, float* sm) {
+    rows = rows_;
+    sc = scale;
+    __syncwarp();
+    for (int g = 0; g < rows; ++g) {
+      const float* src = (const float*)p.a.q + n * p.a.q_token + (row0 + g) * p.a.q_head;
+      for (int e = lane * 4; e < HD; e += 128)
+        *(float4*)(sm + g * HD + e) = e < p.a.E ? *(const float4*)(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < ROWS; ++g) {
+      m[g] = -INFINITY;
+      l[g] = 0.f;
+#pragma unroll
+      for (int x = 0; x < CB; ++x) o[g][x][0] = o[g][x][1] = o[g][x][2] = o[g][x][3] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void step(const PagedAttn& p, uint32_t ks, uint32_t vs, uint32_t seen, int lane, float* sm) {
+    // lanes 2 j and 2 j + 1 of a quarter-warp take the even and odd pieces of one key's row
+    const int half = lane & 1, key = 4 * ((lane >> 1) & 3) + (lane >> 3);
+    float z[ROWS];
+#pragma unroll
+    for (int g = 0; g < ROWS; ++g) z[g] = 0.f;
+    const int pieces = (p.a.E + 3) / 4;
+    for (int i = half; i < pieces; i += 2) {
+      const uint4 u = lds16(ks + key * RB + ((i ^ swizzle(key)) << 4));
+      const float k0 = __uint_as_float(u.x), k1 = __uint_as_float(u.y), k2 = __uint_as_float(u.z), k3 = __uint_as_float(u.w);
+#pragma unroll
+      for (int g = 0; g < ROWS; ++g) {
+        if (g >= rows) break;
+        const float4 q = *(const float4*)(sm + g * HD + 4 * i);
+        z[g] = fmaf(q.x, k0, z[g]);
+        z[g] = fmaf(q.y, k1, z[g]);
+        z[g] = fmaf(q.z, k2, z[g]);
+        z[g] = fmaf(q.w, k3, z[g]);
+      }
+    }
+    const bool on = (seen >> key) & 1;
+    float* ps = sm + ROWS * HD;
+    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < ROWS; ++g) {
+      if (g >= rows) break;
+      float x = z[g] + __shfl_xor_sync(0xffffffffu, z[g], 1);
+      x = on ? x * sc : -INFINITY;
+      float mx = x;
+#pragma unroll
+      for (int o_ = 2; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o_));
+      const float mn = fmaxf(m[g], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[g] - ref);
+      m[g] = mn;
+      const float w = ex2(x - ref);
+      l[g] = l[g] * f + (half ? 0.f : w);
+      if (!half) ps[g * kKeys + key] = w;
+#pragma unroll
+      for (int x2 = 0; x2 < CB; ++x2)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[g][x2][y] *= f;
+    }
+    __syncwarp();
+    for (int j = 0; j < kKeys; j += 4) {
+      float4 w[ROWS];
+#pragma unroll
+      for (int g = 0; g < ROWS; ++g)
+        if (g < rows) w[g] = *(const float4*)(ps + g * kKeys + j);
+#pragma unroll
+      for (int x = 0; x < CB; ++x) {
+        const int d = lane + 32 * x;   // float4 column
+        if (4 * d >= p.a.D) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 u = lds16(vs + (j + k) * RB + ((d ^ swizzle(j + k)) << 4));
+          const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+#pragma unroll
+          for (int g = 0; g < ROWS; ++g) {
+            if (g >= rows) break;
+            const float pw = k == 0 ? w[g].x : k == 1 ? w[g].y : k == 2 ? w[g].z : w[g].w;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[g][x][y] = fmaf(pw, v[y], o[g][x][y]);
+          }
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(float* ml, int lane) {
+#pragma unroll
+    for (int g = 0; g < ROWS; ++g) {
+#pragma unroll
+      for (int o_ = 1; o_ < 32; o_ <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], o_);
+      if (lane == 0) {
+        ml[2 * g] = m[g];
+        ml[2 * g + 1] = l[g];
+      }
+    }
+  }
+  __device__ __forceinline__ void put(float* dst, int part, int lane) {
+#pragma unroll
+    for (int x = 0; x < CB; ++x) {
+      const int d = 4 * (lane + 32 * x);
+      if (d >= HD || d / 64 != part) continue;
+#pragma unroll
+      for (int g = 0; g < ROWS; ++g)
+        *(float4*)(dst + g * 68 + d % 64) = make_float4(o[g][x][0], o[g][x][1], o[g][x][2], o[g][x][3]);
+    }
+  }
+};
+
+// What a CTA leaves for the join kernel about the pair that begins in it and goes on behind it.
+struct Cut {
+  int n, tile, left, slot;   // token (-1: none), head tile, units behind this CTA, the partial's slot here
+};
+struct Parts {
+  float* o;        // [2 grid][ROWS][D]
+  float* ml;       // [2 grid][ROWS][2]
+  Cut* cuts;       // [grid]
+  int64_t* total;  // [1]: the units of the line
+};
+
+// A stage's place in the line, written by the warp that fills it.
+struct alignas(16) Meta {
+  int n, tile;
+  uint32_t seen;   // bits 0..15, 16: first unit of a pair (here), 17: last unit (here)
+  int units;       // of the pair
+};
+
+template <typename Tile, typename C, int HD, int WARPS, int STAGES>
+struct Shape {
+  static constexpr int kUnit = WARPS * kKeys;
+  static constexpr int kStage = 2 * kKeys * HD * (int)sizeof(C);
+  static constexpr int kRing = WARPS * STAGES * kStage;
+  static constexpr int kMerge = WARPS * Tile::ROWS * 68 * 4;
+  static constexpr int kSmem = kRing + kMerge + WARPS * Tile::kSmem;
+};
+
+// Where CTA i's stretch begins: no more CTAs than units work, so that none of them is empty.
+__device__ __forceinline__ int64_t cut_at(int64_t total, int i, int grid) {
+  const int64_t n = total < grid ? total : grid;
+  return i < n ? total * i / n : total;
+}
+
+template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES>
+__global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Parts parts) {
+  using S = Shape<Tile, C, HD, WARPS, STAGES>;
+  constexpr int ROWS = Tile::ROWS, RB = HD * (int)sizeof(C), kThreads = WARPS * 32;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t sums[WARPS];
+  __shared__ int64_t base_s;
+  __shared__ int first_s;
+  __shared__ Meta meta[WARPS][STAGES];
+  __shared__ float ml_s[WARPS][2 * ROWS];
+  // the join kernel may be launched now; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const thin_attn_paged_attention_args& a = p.a;
+  const int G = a.Hq / a.H, tiles = (G + ROWS - 1) / ROWS, HT = a.H * tiles;
+
+  // tokens that see nothing: zeros and -inf
+  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
+    const Token t = token_of<S::kUnit>(p, n);
+    if (!t.live || t.units) continue;
+    for (int i = tid; i < a.Hq * a.D; i += kThreads)
+      ((T*)a.out)[n * a.out_token + (i / a.D) * a.out_head + i % a.D] = elem_of<T>(0.f);
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(int64_t)n * a.Hq + i] = -INFINITY;
+  }
+
+  // this CTA's stretch [lo, hi) of the line and the token that lo lies in
+  const int per = (a.N + kThreads - 1) / kThreads;
+  const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) mine += token_of<S::kUnit>(p, n).units;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) incl += sums[w];
+    total += sums[w];
+  }
+  total *= HT;
+  const int64_t lo = cut_at(total, blockIdx.x, gridDim.x), hi = cut_at(total, blockIdx.x + 1, gridDim.x);
+  if (lo < hi && lo >= (incl - mine) * HT && lo < incl * HT) {
+    int64_t at = (incl - mine) * HT;
+    int n = n0;
+    for (;; ++n) {
+      const int64_t u = (int64_t)token_of<S::kUnit>(p, n).units * HT;
+      if (lo < at + u) break;
+      at += u;
+    }
+    first_s = n;
+    base_s = at;
+  }
+  if (tid == 0) {
+    if (blockIdx.x == 0) *parts.total = total;
+    parts.cuts[blockIdx.x].n = -1;
+  }
+  __syncthreads();
+  const int steps = (int)(hi - lo);
+  if (steps == 0) return;
+
+  // the filling side's place: token, head tile, unit of the pair
+  int n = first_s;
+  Token tok = token_of<S::kUnit>(p, n);
+  int tile = (int)((lo - base_s) / tok.units), unit = (int)((lo - base_s) % tok.units);
+  const int first_unit = unit;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * S::kStage;
+  float* const merge = (float*)(smem + S::kRing);
+  float* const scratch = (float*)(smem + S::kRing + S::kMerge) + warp * (Tile::kSmem / 4);
+  if (a.E < HD) {
+    // the columns behind E are never written again
+    for (int i = lane; i < STAGES * S::kStage / 16; i += 32) *(uint4*)(smem + warp * STAGES * S::kStage + i * 16) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  const bool whole = a.page % kKeys == 0;   // a stage's keys lie on one page
+  const int row_key = lane & (kKeys - 1);
+  int id = -1, off = 0;
+  bool on = false;
+  // the page id of this lane's key at the filling side's place
+  auto look = [&]() {
+    const int key = (tok.start & ~(kKeys - 1)) + unit * S::kUnit + warp * kKeys + row_key;
+    on = key >= tok.start && key < tok.len;
+    const int j = key / a.page;
+    off = key - j * a.page;
+    id = key < tok.len ? tok.ids[(tile / tiles) * p.ids_head + j] : -1;
+  };
+  constexpr int CH = RB / 16;                         // pieces of a stage's row
+  constexpr int LPR = CH < 32 ? CH : 32;              // lanes per row
+  constexpr int RPI = 32 / LPR;                       // rows per instruction
+  const int piece0 = lane % LPR, k_pieces = a.E * (int)sizeof(C) / 16, v_pieces = a.D * (int)sizeof(C) / 16;
+  int filled = 0;
+  auto fill = [&]() {
+    if (filled < steps) {
+      const int st = filled % STAGES, h = tile / tiles;
+      const bool held = id >= 0 && id < a.n_pages;
+      const uint32_t seen = __ballot_sync(0xffffffffu, on && held) & 0xFFFF;
+      const bool first = unit == 0 || filled == 0, last = unit == tok.units - 1 || filled == steps - 1;
+      if (lane == 0) meta[warp][st] = Meta{n, tile, seen | (first ? 1u << 16 : 0) | (last ? 1u << 17 : 0), tok.units};
+      const uint32_t ks = ring + st * S::kStage, vs = ks + kKeys * RB;
+      const int64_t ok = held ? id : 0;
+      const int64_t ko = ok * a.kp_page + h * a.kp_head + off * a.kp_row, vo = ok * a.vp_page + h * a.vp_head + off * a.vp_row;
+      const C* k0 = (const C*)a.k_pages + __shfl_sync(0xffffffffu, ko, 0);
+      const C* v0 = (const C*)a.v_pages + __shfl_sync(0xffffffffu, vo, 0);
+#pragma unroll
+      for (int i = 0; i < kKeys / RPI; ++i) {
+        const int row = i * RPI + lane / LPR;
+        const bool full = (seen >> row) & 1;
+        const C *kr = k0 + row * a.kp_row, *vr = v0 + row * a.vp_row;
+        if (!whole) {
+          kr = (const C*)a.k_pages + __shfl_sync(0xffffffffu, ko, row);
+          vr = (const C*)a.v_pages + __shfl_sync(0xffffffffu, vo, row);
+        }
+#pragma unroll
+        for (int x = 0; x < CH; x += LPR) {
+          const int piece = piece0 + x;
+          const uint32_t at = row * RB + ((piece ^ swizzle(row)) << 4);
+          if (piece < k_pieces) cp16(ks + at, full ? (const char*)kr + piece * 16 : (const char*)a.k_pages, full);
+          if (piece < v_pieces) cp16(vs + at, full ? (const char*)vr + piece * 16 : (const char*)a.v_pages, full);
+        }
+      }
+      ++filled;
+      if (filled < steps) {
+        if (++unit == tok.units) {
+          unit = 0;
+          if (++tile == HT) {
+            tile = 0;
+            do tok = token_of<S::kUnit>(p, ++n);
+            while (tok.units == 0);
+          }
+        }
+        look();
+      }
+    }
+    cp_commit();
+  };
+  look();
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fill();
+
+  Tile t;
+  bool begun_here = false;   // the pair at hand is not the one that the stretch begins in
+  int slot = 0;              // where it leaves a partial
+  for (int s = 0; s < steps; ++s) {
+    cp_wait<STAGES - 2>();
+    __syncwarp();
+    fill();   // the stage that the last step emptied
+    const int st = s % STAGES;
+    const Meta me = meta[warp][st];
+    const int h = me.tile / tiles, g0 = (me.tile % tiles) * ROWS, rows = min(ROWS, G - g0);
+    if (me.seen >> 16 & 1) {
+      begun_here = s > 0;
+      slot = s > 0;
+      t.reset(p, me.n, h * G + g0, rows, p.scale_log2e * (a.k_scale ? a.k_scale[h] : 1.f), lane, scratch);
+    }
+    const uint32_t ks = ring + st * S::kStage;
+    if (me.seen & 0xFFFF) t.step(p, ks, ks + kKeys * RB, me.seen & 0xFFFF, lane, scratch);
+    if (!(me.seen >> 17 & 1)) continue;
+
+    // the pair's end in this CTA: join the warps, and finish the pair or leave a partial
+    const int from = begun_here ? 0 : first_unit, to = s == steps - 1 ? unit : me.units - 1;   // its units here
+    const bool complete = from == 0 && to == me.units - 1;
+    if (from == 0 && !complete && tid == 0) parts.cuts[blockIdx.x] = Cut{me.n, me.tile, me.units - 1 - to, slot};
+    t.finish(ml_s[warp], lane);
+    const float vscale = a.v_scale ? a.v_scale[h] : 1.f;
+    const int64_t part0 = ((int64_t)blockIdx.x * 2 + slot) * ROWS;
+    for (int part = 0; part * 64 < a.D; ++part) {
+      t.put(merge + warp * ROWS * 68, part, lane);
+      __syncthreads();
+      for (int i = tid; i < rows * 16; i += kThreads) {
+        const int g = i >> 4, d = (i & 15) * 4;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml_s[w][2 * g]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float f = ex2(ml_s[w][2 * g] - ref);
+          const float4 y = *(const float4*)(merge + (w * ROWS + g) * 68 + d);
+          l = fmaf(ml_s[w][2 * g + 1], f, l);
+          x.x = fmaf(y.x, f, x.x);
+          x.y = fmaf(y.y, f, x.y);
+          x.z = fmaf(y.z, f, x.z);
+          x.w = fmaf(y.w, f, x.w);
+        }
+        const int col = part * 64 + d;
+        if (complete) {
+          const float inv = l == 0.f ? 0.f : vscale / l;
+          if (col < a.D) {
+            T* out = (T*)a.out + me.n * a.out_token + (h * G + g0 + g) * a.out_head + col;
+            out[0] = elem_of<T>(x.x * inv);
+            out[1] = elem_of<T>(x.y * inv);
+            out[2] = elem_of<T>(x.z * inv);
+            out[3] = elem_of<T>(x.w * inv);
+          }
+          if (part == 0 && d == 0 && a.lse)
+            a.lse[(int64_t)me.n * a.Hq + h * G + g0 + g] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+        } else {
+          if (col < a.D) *(float4*)(parts.o + (part0 + g) * a.D + col) = x;
+          if (part == 0 && d == 0) {
+            parts.ml[2 * (part0 + g)] = mx;
+            parts.ml[2 * (part0 + g) + 1] = l;
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Joins the partials of the pair that begins in CTA blockIdx.x and is cut: four rows per CTA, four
+// warps per row, each taking every fourth partial.
+template <typename T>
+__global__ void __launch_bounds__(512) join_kernel(PagedAttn p, Parts parts, int grid, int ROWS) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const thin_attn_paged_attention_args& a = p.a;
+  const Cut cut = parts.cuts[blockIdx.x];
+  if (cut.n < 0) return;
+  const int G = a.Hq / a.H, tiles = (G + ROWS - 1) / ROWS;
+  const int h = cut.tile / tiles, g0 = (cut.tile % tiles) * ROWS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & 3;
+  const int g = blockIdx.y * 4 + (warp >> 2);
+  __shared__ float o_s[16][256];
+  __shared__ float l_s[16];
+  const bool on = g < min(ROWS, G - g0);
+  // the partials: this CTA's, then slot 0 of those behind it until no unit is left
+  const int64_t total = *parts.total;
+  int n = 1;
+  for (int64_t left = cut.left; left > 0; ++n)
+    left -= cut_at(total, blockIdx.x + n + 1, grid) - cut_at(total, blockIdx.x + n, grid);
+  auto row_of = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i ? 0 : cut.slot)) * ROWS + g; };
+  float m = -INFINITY, l = 0.f;
+  float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (on) {
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, parts.ml[2 * row_of(i)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int i = sub; i < n; i += 4) {
+      const float f = ex2(parts.ml[2 * row_of(i)] - ref);
+      l = fmaf(parts.ml[2 * row_of(i) + 1], f, l);
+      const float* src = parts.o + row_of(i) * a.D;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int d = lane * 4 + 128 * y;
+        if (d < a.D) {
+          const float4 v = *(const float4*)(src + d);
+          x[y].x = fmaf(v.x, f, x[y].x);
+          x[y].y = fmaf(v.y, f, x[y].y);
+          x[y].z = fmaf(v.z, f, x[y].z);
+          x[y].w = fmaf(v.w, f, x[y].w);
+        }
+      }
+    }
+    *(float4*)(o_s[warp] + lane * 4) = x[0];
+    *(float4*)(o_s[warp] + 128 + lane * 4) = x[1];
+    if (lane == 0) l_s[warp] = l;
+  }
+  __syncthreads();
+  if (!on) return;
+  const int w0 = warp & ~3;
+  l = (l_s[w0] + l_s[w0 + 1]) + (l_s[w0 + 2] + l_s[w0 + 3]);
+  const float inv = l == 0.f ? 0.f : (a.v_scale ? a.v_scale[h] : 1.f) / l;
+  T* out = (T*)a.out + cut.n * a.out_token + (h * G + g0 + g) * a.out_head;
+  for (int d = sub * 32 + lane; d < a.D; d += 128)
+    out[d] = elem_of<T>(((o_s[w0][d] + o_s[w0 + 1][d]) + (o_s[w0 + 2][d] + o_s[w0 + 3][d])) * inv);
+  if (sub == 0 && lane == 0 && a.lse)
+    a.lse[(int64_t)cut.n * a.Hq + h * G + g0 + g] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int rows_of(const thin_attn_paged_attention_args& a) {
+  return a.dtype == THIN_ATTN_FP32 || a.Hq / a.H <= 8 ? 8 : 16;
+}
+
+struct PartsLayout {
+  size_t ml, cuts, total, bytes;
+};
+PartsLayout parts_layout(const thin_attn_paged_attention_args& a) {
+  const size_t rows = (size_t)kMaxCtas * 2 * rows_of(a);
+  PartsLayout l;
+  l.ml = al256(rows * a.D * 4);
+  l.cuts = l.ml + al256(rows * 8);
+  l.total = l.cuts + al256(kMaxCtas * sizeof(Cut));
+  l.bytes = l.total + 256;
+  return l;
+}
+
+template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES, int PER_SM>
+cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
+  using S = Shape<Tile, C, HD, WARPS, STAGES>;
+  static_assert((S::kSmem + 3072) * PER_SM <= 227 * 1024, "shared memory");
+  auto kernel = attention_kernel<Tile, T, C, HD, WARPS, STAGES>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const PartsLayout l = parts_layout(p.a);
+  Parts parts{(float*)ws, (float*)((char*)ws + l.ml), (Cut*)((char*)ws + l.cuts), (int64_t*)((char*)ws + l.total)};
+  // no more CTAs than units that the table can hold
+  const int G = p.a.Hq / p.a.H, tiles = (G + Tile::ROWS - 1) / Tile::ROWS;
+  const int64_t per_pair = ((int64_t)p.list_width * p.a.page + S::kUnit - 1) / S::kUnit + 1;
+  const int64_t most = per_pair * p.a.N * p.a.H * tiles;
+  const int grid = (int)(most < 148 * PER_SM ? most : 148 * PER_SM);
+  kernel<<<grid, WARPS * 32, S::kSmem, st>>>(p, parts);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, (Tile::ROWS < G ? Tile::ROWS : G + 3) / 4);
+  cfg.blockDim = dim3(512);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, parts, grid, (int)Tile::ROWS);
+}
+
+template <typename T, int ROWS>
+cudaError_t launch_mma(const PagedAttn& p, void* ws, cudaStream_t st) {
+  const int w = p.a.E > p.a.D ? p.a.E : p.a.D;
+  if (p.a.cache_dtype == THIN_ATTN_E4M3) {
+    if (w <= 128) return launch_tile<MmaTile<T, e4m3, 128, ROWS>, T, e4m3, 128, 4, 5, 2>(p, ws, st);
+    return launch_tile<MmaTile<T, e4m3, 256, ROWS>, T, e4m3, 256, 4, 5, 1>(p, ws, st);
+  }
+  if (w <= 64) return launch_tile<MmaTile<T, T, 64, ROWS>, T, T, 64, 4, 5, 2>(p, ws, st);
+  if (w <= 128) return launch_tile<MmaTile<T, T, 128, ROWS>, T, T, 128, 4, ROWS == 8 ? 3 : 2, 2>(p, ws, st);
+  return launch_tile<MmaTile<T, T, 256, ROWS>, T, T, 256, 4, 3, 1>(p, ws, st);
+}
+
+cudaError_t launch_simt(const PagedAttn& p, void* ws, cudaStream_t st) {
+  const int w = p.a.E > p.a.D ? p.a.E : p.a.D;
+  if (w <= 64) return launch_tile<SimtTile<64>, float, float, 64, 4, 2, 2>(p, ws, st);
+  if (w <= 128) return launch_tile<SimtTile<128>, float, float, 128, 4, 2, 1>(p, ws, st);
+  return launch_tile<SimtTile<256>, float, float, 256, 2, 2, 1>(p, ws, st);
 }
 
 }  // namespace
 
-size_t paged_attention_workspace(const thin_attn_paged_attention_args& a) { return 0; }
+size_t paged_attention_workspace(const thin_attn_paged_attention_args& a) { return parts_layout(a).bytes; }
 
-cudaError_t launch_paged_attention(const PagedAttn& p, void* workspace, cudaStream_t st) {
-  const bool q = p.a.cache_dtype == THIN_ATTN_E4M3;
-  if (p.a.dtype == THIN_ATTN_FP32) return launch_t<float, float>(p, st);
-  if (p.a.dtype == THIN_ATTN_BF16) return q ? launch_t<__nv_bfloat16, e4m3>(p, st) : launch_t<__nv_bfloat16, __nv_bfloat16>(p, st);
-  return q ? launch_t<__half, e4m3>(p, st) : launch_t<__half, __half>(p, st);
+cudaError_t launch_paged_attention(const PagedAttn& p, void* ws, cudaStream_t st) {
+  if (p.a.dtype == THIN_ATTN_FP32) return launch_simt(p, ws, st);
+  const bool few = rows_of(p.a) == 8;
+  if (p.a.dtype == THIN_ATTN_BF16) return few ? launch_mma<__nv_bfloat16, 8>(p, ws, st) : launch_mma<__nv_bfloat16, 16>(p, ws, st);
+  return few ? launch_mma<__half, 8>(p, ws, st) : launch_mma<__half, 16>(p, ws, st);
 }
 
 }  // namespace thin
