@@ -22,6 +22,8 @@ struct PagedAttn {
   int list_width;         // ids per list
   const int32_t* keys;    // (N)
   float scale_log2e;
+  uint32_t page_mul;      // key / page = umulhi(key, page_mul) >> page_shift, page_mul = 0 for page = 1
+  int page_shift;
 };
 size_t paged_attention_workspace(const thin_attn_paged_attention_args& a);
 cudaError_t launch_paged_attention(const PagedAttn& p, void* workspace, cudaStream_t st);

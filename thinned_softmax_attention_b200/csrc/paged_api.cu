@@ -190,6 +190,13 @@ thin_attn_status thin_attn_paged_attention(const thin_attn_paged_attention_args*
   p.a = *a;
   const float sc = a->scale > 0.f ? a->scale : (float)(1.0 / std::sqrt((double)a->E));
   p.scale_log2e = (float)((double)sc * 1.4426950408889634);
+  if (a->page > 1) {
+    // s = ceil(log2 page), mul = ceil(2^(31 + s) / page): off by less than page <= 2^s, so exact below 2^31
+    int s2 = 0;
+    while ((1 << s2) < a->page) ++s2;
+    p.page_mul = (uint32_t)((((uint64_t)1 << (31 + s2)) + a->page - 1) / a->page);
+    p.page_shift = s2 - 1;
+  }
   if (a->top) {
     int32_t* ids = (int32_t*)(ws + l.ids);
     int32_t* keys = (int32_t*)(ws + l.keys);

@@ -44,6 +44,11 @@ struct Token {
   bool live;   // not padding
 };
 
+// key / page for key < 2^31, page <= 65536: by the reciprocal that the host rounded up (PagedAttn).
+__device__ __forceinline__ int page_of(const PagedAttn& p, int key) {
+  return p.page_mul ? (int)(__umulhi((uint32_t)key, p.page_mul) >> p.page_shift) : key;
+}
+
 template <int UNIT>
 __device__ __forceinline__ Token token_of(const PagedAttn& p, int n) {
   Token t;
@@ -60,6 +65,9 @@ __device__ __forceinline__ Token token_of(const PagedAttn& p, int n) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
   const int n = full ? 16 : 0;   // the rest is filled with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -196,15 +204,16 @@ struct MmaTile {
   // One stage: keys at smem address ks, values at vs; bit j of `seen` is key j's.
   __device__ __forceinline__ void step(const PagedAttn& p, uint32_t ks, uint32_t vs, uint32_t seen, int lane, float*) {
     const int r = lane >> 2, c = lane & 3;
-    float s[2][4] = {};
+    float s[2][4] = {}, s2[2][4] = {};   // two chains per tile, for the products' latency
     const uint32_t zero = 0;
+    // column r of S's tile t is key 4 (r >> 1) + 2 t + (r & 1)
+    const uint32_t ka = ks + (4 * (r >> 1) + (r & 1)) * RB + ((c ^ swizzle(4 * (r >> 1) + (r & 1))) << 4);
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
       if (j * 4 * DC >= p.a.E) break;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int row = 4 * (r >> 1) + 2 * t + (r & 1);   // column r of S's tile t
-        const uint4 u = lds16(ks + row * RB + (((c + 4 * j) ^ swizzle(row)) << 4));
+        const uint4 u = lds16((ka ^ ((j & 1) << 6)) + 2 * t * RB + (j >> 1) * 128);
         uint32_t b[QW];
         if constexpr (k8) {
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -223,10 +232,14 @@ struct MmaTile {
         for (int y = 0; y < QW; y += 2) {
           const uint32_t a[4] = {q[j][0][y], ROWS == 16 ? q[j][ROWS / 8 - 1][y] : zero, q[j][0][y + 1],
                                  ROWS == 16 ? q[j][ROWS / 8 - 1][y + 1] : zero};
-          mma<M>(s[t], a, b[y], b[y + 1]);
+          mma<M>(y & 2 ? s2[t] : s[t], a, b[y], b[y + 1]);
         }
       }
     }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[t][x] += s2[t][x];
     // s[t][2 x + u] = row r + 8 x against key 4 c + 2 t + u
     // z is rounded before the maximum is taken, so that z - m is 0 at the maximum, however large both are
 #pragma unroll
@@ -283,14 +296,14 @@ struct MmaTile {
     }
     uint32_t a[4] = {hi[0][0], ROWS == 16 ? hi[ROWS / 8 - 1][0] : lo[0][0], hi[0][1], ROWS == 16 ? hi[ROWS / 8 - 1][1] : lo[0][1]};
     uint32_t a2[4] = {lo[0][0], lo[ROWS / 8 - 1][0], lo[0][1], lo[ROWS / 8 - 1][1]};
+    const uint32_t va = vs + 4 * c * RB + ((r ^ (c << 1)) << 4);
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
       if (i * 8 * DC >= p.a.D) break;
       uint32_t v[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = 4 * c + k;
-        const uint4 u = lds16(vs + row * RB + (((r + 8 * i) ^ swizzle(row)) << 4));
+        const uint4 u = lds16((va ^ ((k & 1) << 6)) + k * RB + i * 128);   // swizzle(4 c + k) = 4 (k & 1) ^ 2 c
         v[k][0] = u.x;
         v[k][1] = u.y;
         v[k][2] = u.z;
@@ -597,48 +610,72 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
   }
   const bool whole = a.page % kKeys == 0;   // a stage's keys lie on one page
   const int row_key = lane & (kKeys - 1);
+  // the filling side's key head
+  const C *k_head, *v_head;
+  const int32_t* ids;
+  auto at_head = [&]() {
+    const int h = tile / tiles;
+    k_head = (const C*)a.k_pages + h * a.kp_head;
+    v_head = (const C*)a.v_pages + h * a.vp_head;
+    ids = tok.ids + h * p.ids_head;
+  };
   int id = -1, off = 0;
   bool on = false;
   // the page id of this lane's key at the filling side's place
   auto look = [&]() {
     const int key = (tok.start & ~(kKeys - 1)) + unit * S::kUnit + warp * kKeys + row_key;
     on = key >= tok.start && key < tok.len;
-    const int j = key / a.page;
+    const int j = page_of(p, key);
     off = key - j * a.page;
-    id = key < tok.len ? tok.ids[(tile / tiles) * p.ids_head + j] : -1;
+    id = key < tok.len ? ids[j] : -1;
   };
-  constexpr int CH = RB / 16;                         // pieces of a stage's row
-  constexpr int LPR = CH < 32 ? CH : 32;              // lanes per row
-  constexpr int RPI = 32 / LPR;                       // rows per instruction
-  const int piece0 = lane % LPR, k_pieces = a.E * (int)sizeof(C) / 16, v_pieces = a.D * (int)sizeof(C) / 16;
+  constexpr int CH = RB / 16;               // pieces of a stage's row
+  constexpr int LPR = CH < 32 ? CH : 32;    // lanes per row
+  constexpr int RPI = 32 / LPR;             // rows per instruction
+  static_assert(RPI == 1 || RPI == 2 || RPI == 4, "");
+  const int r0 = lane / LPR, piece = lane % LPR;
+  const int k_pieces = a.E * (int)sizeof(C) / 16, v_pieces = a.D * (int)sizeof(C) / 16;
+  const uint32_t lane_at = r0 * RB + ((piece ^ ((r0 & 1) << 2)) << 4);
   int filled = 0;
   auto fill = [&]() {
     if (filled < steps) {
-      const int st = filled % STAGES, h = tile / tiles;
+      const int st = filled % STAGES;
       const bool held = id >= 0 && id < a.n_pages;
       const uint32_t seen = __ballot_sync(0xffffffffu, on && held) & 0xFFFF;
       const bool first = unit == 0 || filled == 0, last = unit == tok.units - 1 || filled == steps - 1;
       if (lane == 0) meta[warp][st] = Meta{n, tile, seen | (first ? 1u << 16 : 0) | (last ? 1u << 17 : 0), tok.units};
-      const uint32_t ks = ring + st * S::kStage, vs = ks + kKeys * RB;
-      const int64_t ok = held ? id : 0;
-      const int64_t ko = ok * a.kp_page + h * a.kp_head + off * a.kp_row, vo = ok * a.vp_page + h * a.vp_head + off * a.vp_row;
-      const C* k0 = (const C*)a.k_pages + __shfl_sync(0xffffffffu, ko, 0);
-      const C* v0 = (const C*)a.v_pages + __shfl_sync(0xffffffffu, vo, 0);
+      const uint32_t ks = ring + st * S::kStage;
+      const int64_t page = held ? id : 0;
+      if (whole && seen == 0xFFFF) {
+        // sixteen rows a fixed stride apart
+        const C* kr = k_head + page * a.kp_page + (off - row_key + r0) * a.kp_row + piece * (16 / (int)sizeof(C));
+        const C* vr = v_head + page * a.vp_page + (off - row_key + r0) * a.vp_row + piece * (16 / (int)sizeof(C));
 #pragma unroll
-      for (int i = 0; i < kKeys / RPI; ++i) {
-        const int row = i * RPI + lane / LPR;
-        const bool full = (seen >> row) & 1;
-        const C *kr = k0 + row * a.kp_row, *vr = v0 + row * a.vp_row;
-        if (!whole) {
-          kr = (const C*)a.k_pages + __shfl_sync(0xffffffffu, ko, row);
-          vr = (const C*)a.v_pages + __shfl_sync(0xffffffffu, vo, row);
+        for (int i = 0; i < kKeys / RPI; ++i) {
+          const int row = i * RPI;   // swizzle(row + r0) = swizzle(row) ^ ((r0 & 1) << 2)
+          const uint32_t at = ks + row * RB + (lane_at ^ (swizzle(row) << 4));
+#pragma unroll
+          for (int x = 0; x < CH; x += LPR) {
+            if (piece + x < k_pieces) cp16(at + x * 16, (const char*)kr + x * 16);
+            if (piece + x < v_pieces) cp16(at + kKeys * RB + x * 16, (const char*)vr + x * 16);
+          }
+          kr += RPI * a.kp_row;
+          vr += RPI * a.vp_row;
         }
+      } else {
+        const int64_t ko = page * a.kp_page + off * a.kp_row, vo = page * a.vp_page + off * a.vp_row;
 #pragma unroll
-        for (int x = 0; x < CH; x += LPR) {
-          const int piece = piece0 + x;
-          const uint32_t at = row * RB + ((piece ^ swizzle(row)) << 4);
-          if (piece < k_pieces) cp16(ks + at, full ? (const char*)kr + piece * 16 : (const char*)a.k_pages, full);
-          if (piece < v_pieces) cp16(vs + at, full ? (const char*)vr + piece * 16 : (const char*)a.v_pages, full);
+        for (int i = 0; i < kKeys / RPI; ++i) {
+          const int row = i * RPI + r0;
+          const bool full = (seen >> row) & 1;
+          const C *kr = k_head + __shfl_sync(0xffffffffu, ko, row), *vr = v_head + __shfl_sync(0xffffffffu, vo, row);
+          const uint32_t at = ks + i * RPI * RB + (lane_at ^ (swizzle(i * RPI) << 4));
+#pragma unroll
+          for (int x = 0; x < CH; x += LPR) {
+            if (piece + x < k_pieces) cp16(at + x * 16, full ? (const char*)kr + (piece + x) * 16 : (const char*)a.k_pages, full);
+            if (piece + x < v_pieces)
+              cp16(at + kKeys * RB + x * 16, full ? (const char*)vr + (piece + x) * 16 : (const char*)a.v_pages, full);
+          }
         }
       }
       ++filled;
@@ -650,12 +687,14 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
             do tok = token_of<S::kUnit>(p, ++n);
             while (tok.units == 0);
           }
+          at_head();
         }
         look();
       }
     }
     cp_commit();
   };
+  at_head();
   look();
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) fill();
