@@ -35,7 +35,7 @@ namespace thin {
 namespace {
 
 constexpr int kKeys = 16;          // keys of a warp's stage
-constexpr int kMaxCtas = 296;      // 148 SMs x 2
+constexpr int kMaxCtas = 444;      // 148 SMs x 3
 
 // One token of the call: its row of outputs, its visible keys [start, len) and their units.
 struct Token {
@@ -50,16 +50,19 @@ __device__ __forceinline__ int page_of(const PagedAttn& p, int key) {
 }
 
 template <int UNIT>
-__device__ __forceinline__ Token token_of(const PagedAttn& p, int n) {
+__device__ __forceinline__ Token token_from(const PagedAttn& p, int n, int row, int len) {
   Token t;
-  const int row = p.a.rows ? p.a.rows[n] : n;
   t.live = row >= 0 && row < p.a.R;
-  t.len = t.live ? min(max(p.keys[n], 0), p.list_width * p.a.page) : 0;
+  t.len = t.live ? min(max(len, 0), p.list_width * p.a.page) : 0;
   t.start = p.a.window && t.len > p.a.window ? t.len - p.a.window : 0;
   const int first = t.start & ~(kKeys - 1);
   t.units = (t.len - first + UNIT - 1) / UNIT;
   t.ids = p.ids + (p.list_rows ? row : n) * p.ids_token;
   return t;
+}
+template <int UNIT>
+__device__ __forceinline__ Token token_of(const PagedAttn& p, int n) {
+  return token_from<UNIT>(p, n, p.a.rows ? p.a.rows[n] : n, p.keys[n]);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
@@ -117,10 +120,9 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 values as two fp16 ones (exact).
-__device__ __forceinline__ uint32_t widen2(uint32_t b) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)b, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 values as fp16 ones (exact), two to a word.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }" : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -140,30 +142,38 @@ struct MmaTile {
   static_assert(ROWS == 8 || ROWS == 16, "");
   static_assert(VI >= 1 && KJ == 2 * VI, "");
 
-  uint32_t q[KJ][ROWS / 8][QW];
+  uint32_t q[KJ][ROWS / 8][QW], next[KJ][ROWS / 8][QW];
   float o[VI][DC][4];
   float m[2], l[2], sc[2];
 
-  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float*) {
+  // Query rows are fetched a step before the pair that they belong to, where the registers allow it.
+  static constexpr bool kAhead = HD <= 128 && !k8;
+  __device__ __forceinline__ void fetch(const PagedAttn& p, int n, int row0, int rows, int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int x = 0; x < ROWS / 8; ++x) {
       const int g = r + 8 * x;
       const T* src = (const T*)p.a.q + n * p.a.q_token + (row0 + g) * p.a.q_head;
-      uint32_t w[KJ][QW];
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
         const int e = (c + 4 * j) * DC;
 #pragma unroll
-        for (int y = 0; y < QW / 4; ++y) {
+        for (int y = 0; y < QW; y += 4) {
           uint4 u = make_uint4(0, 0, 0, 0);
-          if (g < rows && e < p.a.E) u = ((const uint4*)(src + e))[y];
-          w[j][4 * y] = u.x;
-          w[j][4 * y + 1] = u.y;
-          w[j][4 * y + 2] = u.z;
-          w[j][4 * y + 3] = u.w;
+          if (g < rows && e < p.a.E) u = ((const uint4*)(src + e))[y / 4];
+          next[j][x][y] = u.x;
+          next[j][x][y + 1] = u.y;
+          next[j][x][y + 2] = u.z;
+          next[j][x][y + 3] = u.w;
         }
       }
+    }
+  }
+
+  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float*) {
+    if constexpr (!kAhead) fetch(p, n, row0, rows, lane);
+#pragma unroll
+    for (int x = 0; x < ROWS / 8; ++x) {
       sc[x] = scale;
       if constexpr (k8 && !std::is_same<T, __half>::value) {
         // q into fp16, times the power of two that brings the row's largest value to 2^13 .. 2^14: what
@@ -173,7 +183,7 @@ struct MmaTile {
         for (int j = 0; j < KJ; ++j)
 #pragma unroll
           for (int y = 0; y < QW; ++y) {
-            const float2 f = unpack2<T>(w[j][y]);
+            const float2 f = unpack2<T>(next[j][x][y]);
             mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -183,15 +193,16 @@ struct MmaTile {
         for (int j = 0; j < KJ; ++j)
 #pragma unroll
           for (int y = 0; y < QW; ++y) {
-            const float2 f = unpack2<T>(w[j][y]);
-            w[j][y] = pack2<__half>(f.x * pow2f(up), f.y * pow2f(up));
+            const float2 f = unpack2<T>(next[j][x][y]);
+            q[j][x][y] = pack2<__half>(f.x * pow2f(up), f.y * pow2f(up));
           }
         sc[x] = scale * pow2f(-up);
+      } else {
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+          for (int y = 0; y < QW; ++y) q[j][x][y] = next[j][x][y];
       }
-#pragma unroll
-      for (int j = 0; j < KJ; ++j)
-#pragma unroll
-        for (int y = 0; y < QW; ++y) q[j][x][y] = w[j][y];
       m[x] = -INFINITY;
       l[x] = 0.f;
     }
@@ -218,10 +229,7 @@ struct MmaTile {
         if constexpr (k8) {
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            b[2 * y] = widen2(w[y] & 0xFFFF);
-            b[2 * y + 1] = widen2(w[y] >> 16);
-          }
+          for (int y = 0; y < 4; ++y) widen4(w[y], b[2 * y], b[2 * y + 1]);
         } else {
           b[0] = u.x;
           b[1] = u.y;
@@ -317,11 +325,11 @@ struct MmaTile {
             // bytes 2 y and 2 y + 1 of the word, those of two keys side by side
             const uint32_t b0 = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
             const uint32_t b1 = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t p0 = widen2(z ? b0 >> 16 : b0 & 0xFFFF), p1 = widen2(z ? b1 >> 16 : b1 & 0xFFFF);
-              mma<M>(o[i][4 * w + 2 * y + z], a, p0, p1);
-            }
+            uint32_t p0[2], p1[2];
+            widen4(b0, p0[0], p0[1]);
+            widen4(b1, p1[0], p1[1]);
+            mma<M>(o[i][4 * w + 2 * y], a, p0[0], p1[0]);
+            mma<M>(o[i][4 * w + 2 * y + 1], a, p0[1], p1[1]);
           }
         } else {
 #pragma unroll
@@ -348,25 +356,28 @@ struct MmaTile {
       }
     }
   }
-  // Columns [64 part, 64 part + 64) of o into dst (ROWS x 68).
-  __device__ __forceinline__ void put(float* dst, int part, int lane) {
+  // Columns [COLS part, COLS part + COLS) of o into dst (ROWS x COLS).
+  static constexpr int COLS = ROWS == 8 && HD > 64 ? 128 : 64;
+  static __device__ __forceinline__ int place(int g, int col) {   // float4 `col` of row g: quarter-warps meet every bank once
+    return g * (COLS / 4) + (col ^ ((col >> 3) & 3) ^ ((g & 1) << (k8 ? 2 : 1)));
+  }
+  __device__ __forceinline__ void put(float4* dst, int part, int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int i = 0; i < VI; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int d = DC * (2 * c + u + 8 * i);
+        if (d / COLS != part) continue;
 #pragma unroll
         for (int y = 0; y < DC; y += 4) {
-          if ((d + y) / 64 != part) continue;
+          const int col = (d % COLS + y) / 4;
           if constexpr (ROWS == 8) {
-            float4 x = make_float4(o[i][y][u] + o[i][y][2 + u], o[i][y + 1][u] + o[i][y + 1][2 + u],
-                                   o[i][y + 2][u] + o[i][y + 2][2 + u], o[i][y + 3][u] + o[i][y + 3][2 + u]);
-            *(float4*)(dst + r * 68 + (d + y) % 64) = x;
+            dst[place(r, col)] = make_float4(o[i][y][u] + o[i][y][2 + u], o[i][y + 1][u] + o[i][y + 1][2 + u],
+                                             o[i][y + 2][u] + o[i][y + 2][2 + u], o[i][y + 3][u] + o[i][y + 3][2 + u]);
           } else {
-            *(float4*)(dst + r * 68 + (d + y) % 64) = make_float4(o[i][y][u], o[i][y + 1][u], o[i][y + 2][u], o[i][y + 3][u]);
-            *(float4*)(dst + (r + 8) * 68 + (d + y) % 64) =
-                make_float4(o[i][y][2 + u], o[i][y + 1][2 + u], o[i][y + 2][2 + u], o[i][y + 3][2 + u]);
+            dst[place(r, col)] = make_float4(o[i][y][u], o[i][y + 1][u], o[i][y + 2][u], o[i][y + 3][u]);
+            dst[place(r + 8, col)] = make_float4(o[i][y][2 + u], o[i][y + 1][2 + u], o[i][y + 2][2 + u], o[i][y + 3][2 + u]);
           }
         }
       }
@@ -379,6 +390,7 @@ struct MmaTile {
 template <int HD>
 struct SimtTile {
   static constexpr int ROWS = 8;
+  static constexpr bool kAhead = false;
   static constexpr int RB = HD * 4;
   static constexpr int CB = HD > 128 ? HD / 128 : 1;          // float4 columns per lane
   static constexpr int kSmem = (ROWS * HD + ROWS * kKeys) * 4;   // q and p of a warp
@@ -484,34 +496,34 @@ struct SimtTile {
       }
     }
   }
-  __device__ __forceinline__ void put(float* dst, int part, int lane) {
+  static constexpr int COLS = HD > 64 ? 128 : 64;
+  static __device__ __forceinline__ int place(int g, int col) { return g * (COLS / 4) + col; }
+  __device__ __forceinline__ void put(float4* dst, int part, int lane) {
 #pragma unroll
     for (int x = 0; x < CB; ++x) {
       const int d = 4 * (lane + 32 * x);
-      if (d >= HD || d / 64 != part) continue;
+      if (d >= HD || d / COLS != part) continue;
 #pragma unroll
-      for (int g = 0; g < ROWS; ++g)
-        *(float4*)(dst + g * 68 + d % 64) = make_float4(o[g][x][0], o[g][x][1], o[g][x][2], o[g][x][3]);
+      for (int g = 0; g < ROWS; ++g) dst[place(g, d % COLS / 4)] = make_float4(o[g][x][0], o[g][x][1], o[g][x][2], o[g][x][3]);
     }
   }
 };
 
 // What a CTA leaves for the join kernel about the pair that begins in it and goes on behind it.
 struct Cut {
-  int n, tile, left, slot;   // token (-1: none), head tile, units behind this CTA, the partial's slot here
+  int n, tile, last, slot;   // token (-1: none), head tile, the CTA that it ends in, the partial's slot here
 };
 struct Parts {
   float* o;        // [2 grid][ROWS][D]
   float* ml;       // [2 grid][ROWS][2]
   Cut* cuts;       // [grid]
-  int64_t* total;  // [1]: the units of the line
 };
 
 // A stage's place in the line, written by the warp that fills it.
 struct alignas(16) Meta {
   int n, tile;
   uint32_t seen;   // bits 0..15, 16: first unit of a pair (here), 17: last unit (here)
-  int units;       // of the pair
+  int left;        // units of the pair behind it
 };
 
 template <typename Tile, typename C, int HD, int WARPS, int STAGES>
@@ -519,24 +531,27 @@ struct Shape {
   static constexpr int kUnit = WARPS * kKeys;
   static constexpr int kStage = 2 * kKeys * HD * (int)sizeof(C);
   static constexpr int kRing = WARPS * STAGES * kStage;
-  static constexpr int kMerge = WARPS * Tile::ROWS * 68 * 4;
+  static constexpr int kMerge = WARPS * Tile::ROWS * Tile::COLS * 4;
   static constexpr int kSmem = kRing + kMerge + WARPS * Tile::kSmem;
 };
 
-// Where CTA i's stretch begins: no more CTAs than units work, so that none of them is empty.
-__device__ __forceinline__ int64_t cut_at(int64_t total, int i, int grid) {
-  const int64_t n = total < grid ? total : grid;
-  return i < n ? total * i / n : total;
-}
+// A place on the line.
+struct End {
+  int n, tile, unit;
+};
 
-template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES>
-__global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Parts parts) {
+// A pair's stretch of the line: its units, and kPairCost more before them for what a pair costs besides
+// its keys (the join of the warps, the outputs), in units.  Without them a stretch full of short
+// requests takes several times as long as one within a long request.
+constexpr int kPairCost = 2;
+
+template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES, int PER_SM>
+__global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn p, Parts parts) {
   using S = Shape<Tile, C, HD, WARPS, STAGES>;
   constexpr int ROWS = Tile::ROWS, RB = HD * (int)sizeof(C), kThreads = WARPS * 32;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t sums[WARPS];
-  __shared__ int64_t base_s;
-  __shared__ int first_s;
+  __shared__ End ends_s[2];
   __shared__ Meta meta[WARPS][STAGES];
   __shared__ float ml_s[WARPS][2 * ROWS];
   // the join kernel may be launched now; it waits for this grid's end before it reads
@@ -555,11 +570,13 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
       for (int i = tid; i < a.Hq; i += kThreads) a.lse[(int64_t)n * a.Hq + i] = -INFINITY;
   }
 
-  // this CTA's stretch [lo, hi) of the line and the token that lo lies in
+  // this CTA's stretch [lo, hi) of the line: every thread adds up some tokens, and the threads whose
+  // tokens hold lo and hi find the places there
   const int per = (a.N + kThreads - 1) / kThreads;
   const int n0 = min(a.N, tid * per), n1 = min(a.N, n0 + per);
+  auto length = [&](int units) { return units ? (int64_t)(units + kPairCost) * HT : 0; };
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += token_of<S::kUnit>(p, n).units;
+  for (int n = n0; n < n1; ++n) mine += length(token_of<S::kUnit>(p, n).units);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -567,6 +584,7 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
     if (lane >= o) incl += y;
   }
   if (lane == 31) sums[warp] = incl;
+  if (tid == 0) parts.cuts[blockIdx.x].n = -1;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
@@ -574,34 +592,42 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
     if (w < warp) incl += sums[w];
     total += sums[w];
   }
-  total *= HT;
-  const int64_t lo = cut_at(total, blockIdx.x, gridDim.x), hi = cut_at(total, blockIdx.x + 1, gridDim.x);
-  if (lo < hi && lo >= (incl - mine) * HT && lo < incl * HT) {
-    int64_t at = (incl - mine) * HT;
-    int n = n0;
-    for (;; ++n) {
-      const int64_t u = (int64_t)token_of<S::kUnit>(p, n).units * HT;
-      if (lo < at + u) break;
-      at += u;
+  const int64_t ctas = min(total, (int64_t)gridDim.x);   // no stretch is empty
+  if (blockIdx.x >= ctas) return;
+  const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t x = i ? hi - 1 : lo;   // the stretch's first and last place
+    if (x < incl - mine || x >= incl) continue;
+    int64_t at = incl - mine;
+    for (int n = n0;; ++n) {
+      const int units = token_of<S::kUnit>(p, n).units;
+      if (x < at + length(units)) {
+        const int in = (int)((x - at) % (units + kPairCost)) - kPairCost;   // negative: before the pair's units
+        ends_s[i] = End{n, (int)((x - at) / (units + kPairCost)), i ? in : max(in, 0)};
+        break;
+      }
+      at += length(units);
     }
-    first_s = n;
-    base_s = at;
-  }
-  if (tid == 0) {
-    if (blockIdx.x == 0) *parts.total = total;
-    parts.cuts[blockIdx.x].n = -1;
   }
   __syncthreads();
-  const int steps = (int)(hi - lo);
-  if (steps == 0) return;
+  const End end = ends_s[1];   // the last place: unit `unit` of the pair, -1 or less: none of its units
 
   // the filling side's place: token, head tile, unit of the pair
-  int n = first_s;
-  Token tok = token_of<S::kUnit>(p, n);
-  int tile = (int)((lo - base_s) / tok.units), unit = (int)((lo - base_s) % tok.units);
+  int n = ends_s[0].n, tile = ends_s[0].tile, unit = ends_s[0].unit;
   const int first_unit = unit;
+  Token tok = token_of<S::kUnit>(p, n);
+  int raw_row, raw_len;   // of the token behind it, fetched ahead
+  auto peek = [&]() {
+    const int next = min(n + 1, a.N - 1);
+    raw_row = a.rows ? a.rows[next] : next;
+    raw_len = p.keys[next];
+  };
+  peek();
+  // whether the filling side has come to the stretch's end
+  auto ended = [&]() { return n > end.n || (n == end.n && (tile > end.tile || (tile == end.tile && unit > end.unit))); };
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * S::kStage;
-  float* const merge = (float*)(smem + S::kRing);
+  float4* const merge = (float4*)(smem + S::kRing);
   float* const scratch = (float*)(smem + S::kRing + S::kMerge) + warp * (Tile::kSmem / 4);
   if (a.E < HD) {
     // the columns behind E are never written again
@@ -637,13 +663,12 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
   const int k_pieces = a.E * (int)sizeof(C) / 16, v_pieces = a.D * (int)sizeof(C) / 16;
   const uint32_t lane_at = r0 * RB + ((piece ^ ((r0 & 1) << 2)) << 4);
   int filled = 0;
+  bool more = !ended();
   auto fill = [&]() {
-    if (filled < steps) {
+    if (more) {
       const int st = filled % STAGES;
       const bool held = id >= 0 && id < a.n_pages;
       const uint32_t seen = __ballot_sync(0xffffffffu, on && held) & 0xFFFF;
-      const bool first = unit == 0 || filled == 0, last = unit == tok.units - 1 || filled == steps - 1;
-      if (lane == 0) meta[warp][st] = Meta{n, tile, seen | (first ? 1u << 16 : 0) | (last ? 1u << 17 : 0), tok.units};
       const uint32_t ks = ring + st * S::kStage;
       const int64_t page = held ? id : 0;
       if (whole && seen == 0xFFFF) {
@@ -678,58 +703,70 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
           }
         }
       }
+      Meta me{n, tile, seen | (unit == 0 || filled == 0 ? 1u << 16 : 0), tok.units - 1 - unit};
       ++filled;
-      if (filled < steps) {
-        if (++unit == tok.units) {
-          unit = 0;
-          if (++tile == HT) {
-            tile = 0;
-            do tok = token_of<S::kUnit>(p, ++n);
-            while (tok.units == 0);
+      if (++unit == tok.units) {
+        unit = 0;
+        if (++tile == HT) {
+          tile = 0;
+          while (++n < a.N) {
+            tok = token_from<S::kUnit>(p, n, raw_row, raw_len);
+            peek();
+            if (tok.units) break;
           }
-          at_head();
         }
-        look();
+        at_head();
       }
+      more = !ended();
+      if (more) look();
+      if (me.left == 0 || !more) me.seen |= 1u << 17;
+      if (lane == 0) meta[warp][st] = me;
     }
     cp_commit();
   };
   at_head();
-  look();
+  if (more) look();
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) fill();
 
   Tile t;
-  bool begun_here = false;   // the pair at hand is not the one that the stretch begins in
-  int slot = 0;              // where it leaves a partial
-  for (int s = 0; s < steps; ++s) {
+  int slot = 0;   // 0: the pair at hand is the one that the stretch begins in, 1: a later one
+  auto fetch = [&](const Meta& me) {
+    const int h = me.tile / tiles, g0 = (me.tile % tiles) * ROWS;
+    if constexpr (Tile::kAhead) t.fetch(p, me.n, h * G + g0, min(ROWS, G - g0), lane);
+  };
+  __syncwarp();
+  if (filled) fetch(meta[warp][0]);
+  for (int s = 0; s < filled; ++s) {
     cp_wait<STAGES - 2>();
     __syncwarp();
     fill();   // the stage that the last step emptied
+    __syncwarp();
     const int st = s % STAGES;
     const Meta me = meta[warp][st];
     const int h = me.tile / tiles, g0 = (me.tile % tiles) * ROWS, rows = min(ROWS, G - g0);
     if (me.seen >> 16 & 1) {
-      begun_here = s > 0;
       slot = s > 0;
       t.reset(p, me.n, h * G + g0, rows, p.scale_log2e * (a.k_scale ? a.k_scale[h] : 1.f), lane, scratch);
     }
+    if (s + 1 < filled && (meta[warp][(s + 1) % STAGES].seen >> 16 & 1)) fetch(meta[warp][(s + 1) % STAGES]);
     const uint32_t ks = ring + st * S::kStage;
     if (me.seen & 0xFFFF) t.step(p, ks, ks + kKeys * RB, me.seen & 0xFFFF, lane, scratch);
     if (!(me.seen >> 17 & 1)) continue;
 
     // the pair's end in this CTA: join the warps, and finish the pair or leave a partial
-    const int from = begun_here ? 0 : first_unit, to = s == steps - 1 ? unit : me.units - 1;   // its units here
-    const bool complete = from == 0 && to == me.units - 1;
-    if (from == 0 && !complete && tid == 0) parts.cuts[blockIdx.x] = Cut{me.n, me.tile, me.units - 1 - to, slot};
+    const bool begins = slot || first_unit == 0, complete = begins && me.left == 0;
+    if (begins && !complete && tid == 0)   // the pair's end on the line, and the CTA whose stretch holds it
+      parts.cuts[blockIdx.x] = Cut{me.n, me.tile, (int)(((hi + me.left) * ctas - 1) / total), slot};
     t.finish(ml_s[warp], lane);
     const float vscale = a.v_scale ? a.v_scale[h] : 1.f;
     const int64_t part0 = ((int64_t)blockIdx.x * 2 + slot) * ROWS;
-    for (int part = 0; part * 64 < a.D; ++part) {
-      t.put(merge + warp * ROWS * 68, part, lane);
+    constexpr int COLS = Tile::COLS;
+    for (int part = 0; part * COLS < a.D; ++part) {
+      t.put(merge + warp * ROWS * (COLS / 4), part, lane);
       __syncthreads();
-      for (int i = tid; i < rows * 16; i += kThreads) {
-        const int g = i >> 4, d = (i & 15) * 4;
+      for (int i = tid; i < rows * (COLS / 4); i += kThreads) {
+        const int g = i / (COLS / 4), d = i % (COLS / 4);
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml_s[w][2 * g]);
@@ -739,14 +776,14 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
           const float f = ex2(ml_s[w][2 * g] - ref);
-          const float4 y = *(const float4*)(merge + (w * ROWS + g) * 68 + d);
+          const float4 y = merge[w * ROWS * (COLS / 4) + Tile::place(g, d)];
           l = fmaf(ml_s[w][2 * g + 1], f, l);
           x.x = fmaf(y.x, f, x.x);
           x.y = fmaf(y.y, f, x.y);
           x.z = fmaf(y.z, f, x.z);
           x.w = fmaf(y.w, f, x.w);
         }
-        const int col = part * 64 + d;
+        const int col = part * COLS + 4 * d;
         if (complete) {
           const float inv = l == 0.f ? 0.f : vscale / l;
           if (col < a.D) {
@@ -774,7 +811,7 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(PagedAttn p, Part
 // Joins the partials of the pair that begins in CTA blockIdx.x and is cut: four rows per CTA, four
 // warps per row, each taking every fourth partial.
 template <typename T>
-__global__ void __launch_bounds__(512) join_kernel(PagedAttn p, Parts parts, int grid, int ROWS) {
+__global__ void __launch_bounds__(512) join_kernel(PagedAttn p, Parts parts, int ROWS) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const thin_attn_paged_attention_args& a = p.a;
   const Cut cut = parts.cuts[blockIdx.x];
@@ -786,11 +823,7 @@ __global__ void __launch_bounds__(512) join_kernel(PagedAttn p, Parts parts, int
   __shared__ float o_s[16][256];
   __shared__ float l_s[16];
   const bool on = g < min(ROWS, G - g0);
-  // the partials: this CTA's, then slot 0 of those behind it until no unit is left
-  const int64_t total = *parts.total;
-  int n = 1;
-  for (int64_t left = cut.left; left > 0; ++n)
-    left -= cut_at(total, blockIdx.x + n + 1, grid) - cut_at(total, blockIdx.x + n, grid);
+  const int n = cut.last - (int)blockIdx.x + 1;   // the partials: this CTA's, then slot 0 of those behind it
   auto row_of = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i ? 0 : cut.slot)) * ROWS + g; };
   float m = -INFINITY, l = 0.f;
   float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -839,27 +872,26 @@ int rows_of(const thin_attn_paged_attention_args& a) {
 }
 
 struct PartsLayout {
-  size_t ml, cuts, total, bytes;
+  size_t ml, cuts, bytes;
 };
 PartsLayout parts_layout(const thin_attn_paged_attention_args& a) {
   const size_t rows = (size_t)kMaxCtas * 2 * rows_of(a);
   PartsLayout l;
   l.ml = al256(rows * a.D * 4);
   l.cuts = l.ml + al256(rows * 8);
-  l.total = l.cuts + al256(kMaxCtas * sizeof(Cut));
-  l.bytes = l.total + 256;
+  l.bytes = l.cuts + al256(kMaxCtas * sizeof(Cut));
   return l;
 }
 
 template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES, int PER_SM>
 cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
   using S = Shape<Tile, C, HD, WARPS, STAGES>;
-  static_assert((S::kSmem + 3072) * PER_SM <= 227 * 1024, "shared memory");
-  auto kernel = attention_kernel<Tile, T, C, HD, WARPS, STAGES>;
+  static_assert((S::kSmem + 2048) * PER_SM <= 228 * 1024, "shared memory: with what the kernel declares and 1 KB of the driver's");
+  auto kernel = attention_kernel<Tile, T, C, HD, WARPS, STAGES, PER_SM>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   const PartsLayout l = parts_layout(p.a);
-  Parts parts{(float*)ws, (float*)((char*)ws + l.ml), (Cut*)((char*)ws + l.cuts), (int64_t*)((char*)ws + l.total)};
+  Parts parts{(float*)ws, (float*)((char*)ws + l.ml), (Cut*)((char*)ws + l.cuts)};
   // no more CTAs than units that the table can hold
   const int G = p.a.Hq / p.a.H, tiles = (G + Tile::ROWS - 1) / Tile::ROWS;
   const int64_t per_pair = ((int64_t)p.list_width * p.a.page + S::kUnit - 1) / S::kUnit + 1;
@@ -877,18 +909,18 @@ cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, parts, grid, (int)Tile::ROWS);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, parts, (int)Tile::ROWS);
 }
 
 template <typename T, int ROWS>
 cudaError_t launch_mma(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int w = p.a.E > p.a.D ? p.a.E : p.a.D;
   if (p.a.cache_dtype == THIN_ATTN_E4M3) {
-    if (w <= 128) return launch_tile<MmaTile<T, e4m3, 128, ROWS>, T, e4m3, 128, 4, 5, 2>(p, ws, st);
-    return launch_tile<MmaTile<T, e4m3, 256, ROWS>, T, e4m3, 256, 4, 5, 1>(p, ws, st);
+    if (w <= 128) return launch_tile<MmaTile<T, e4m3, 128, ROWS>, T, e4m3, 128, 4, 3, 3>(p, ws, st);
+    return launch_tile<MmaTile<T, e4m3, 256, ROWS>, T, e4m3, 256, 4, 3, 2>(p, ws, st);
   }
   if (w <= 64) return launch_tile<MmaTile<T, T, 64, ROWS>, T, T, 64, 4, 5, 2>(p, ws, st);
-  if (w <= 128) return launch_tile<MmaTile<T, T, 128, ROWS>, T, T, 128, 4, ROWS == 8 ? 3 : 2, 2>(p, ws, st);
+  if (w <= 128) return launch_tile<MmaTile<T, T, 128, ROWS>, T, T, 128, 4, 3, 2>(p, ws, st);
   return launch_tile<MmaTile<T, T, 256, ROWS>, T, T, 256, 4, 3, 1>(p, ws, st);
 }
 
