@@ -20,6 +20,7 @@ struct PagedAttn {
   int64_t ids_token, ids_head;
   int list_rows;          // 1: list(n) = rows[n], 0: list(n) = n
   int list_width;         // ids per list
+  bool follows;           // launched behind the selection on the same stream: may be set up while that runs
   const int32_t* keys;    // (N)
   float scale_log2e;
   uint32_t page_mul;      // key / page = umulhi(key, page_mul) >> page_shift, page_mul = 0 for page = 1
@@ -30,8 +31,7 @@ cudaError_t launch_paged_attention(const PagedAttn& p, void* workspace, cudaStre
 
 // Page selection: per token and key head the chosen pages' ids (lists of `top`), and per token the
 // keys they hold.
-size_t paged_select_workspace(const thin_attn_paged_attention_args& a);
-cudaError_t launch_paged_select(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, void* workspace,
-                                cudaStream_t st);
+bool paged_select_fits(const thin_attn_paged_attention_args& a);   // scores and queries in shared memory
+cudaError_t launch_paged_select(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, cudaStream_t st);
 
 }  // namespace thin

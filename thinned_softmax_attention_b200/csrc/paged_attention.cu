@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
   __shared__ float ml_s[WARPS][2 * ROWS];
   // the join kernel may be launched now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (p.follows) asm volatile("griddepcontrol.wait;" ::: "memory");   // for the selected lists
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const thin_attn_paged_attention_args& a = p.a;
   const int G = a.Hq / a.H, tiles = (G + ROWS - 1) / ROWS, HT = a.H * tiles;
@@ -897,18 +898,22 @@ cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int64_t per_pair = ((int64_t)p.list_width * p.a.page + S::kUnit - 1) / S::kUnit + 1;
   const int64_t most = per_pair * p.a.N * p.a.H * tiles;
   const int grid = (int)(most < 148 * PER_SM ? most : 148 * PER_SM);
-  kernel<<<grid, WARPS * 32, S::kSmem, st>>>(p, parts);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid, (Tile::ROWS < G ? Tile::ROWS : G + 3) / 4);
-  cfg.blockDim = dim3(512);
   cfg.stream = st;
   cfg.attrs = attr;
+  cfg.numAttrs = p.follows ? 1 : 0;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = S::kSmem;
+  e = cudaLaunchKernelEx(&cfg, kernel, p, parts);
+  if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(grid, (Tile::ROWS < G ? Tile::ROWS : G + 3) / 4);
+  cfg.blockDim = dim3(512);
   return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, parts, (int)Tile::ROWS);
 }
 
