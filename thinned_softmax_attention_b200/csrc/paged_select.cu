@@ -11,9 +11,11 @@
 // bytes, straight from global memory; each is read once.
 //
 // A cluster of CTAs serves one (token, key head), each an equal run of its pages, the scores in shared
-// memory.  The top-th largest is found by four rounds of an 8-bit radix search whose
-// histograms the CTAs read from one another; then each writes its pages above the threshold, and the
-// first of those on it, behind those of the CTAs before it, so the lists ascend.
+// memory as words of the same order.  The smallest word taken is found by a radix search, 10 bits a
+// round from the leading bit of (largest - smallest word), with histograms that the CTAs read from
+// one another; it ends as soon as a bin is taken whole, mostly in the second round.  Then each CTA writes
+// its pages above that word, and the first of those on it, behind the pages of the CTAs before it, so
+// the lists ascend.
 #include <cooperative_groups.h>
 
 #include "paged.h"
@@ -28,7 +30,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kPerSm = 4;
+constexpr int kMostPages = 4096;   // of a CTA, where a larger cluster can be had
 constexpr int kGroup = 8;   // pages of one product
+constexpr int kBins = 1024;
 
 // Token n's request and the pages its keys reach; false for padding.
 __device__ __forceinline__ bool token_pages(const thin_attn_paged_attention_args& a, int n, int* row, int* len, int* pages) {
@@ -39,7 +44,7 @@ __device__ __forceinline__ bool token_pages(const thin_attn_paged_attention_args
   return true;
 }
 
-// Larger scores give larger words; no score gives 0xFFFFFFFF, the word of a forced page.
+// Larger scores give larger words.
 __device__ __forceinline__ uint32_t rank_of(float s) {
   const uint32_t u = __float_as_uint(s);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -92,7 +97,7 @@ __device__ __forceinline__ void round_queries(const thin_attn_paged_attention_ar
 }
 
 template <typename T, int KJ>   // KJ: 16-byte pieces per lane and page, 2 E <= 64 KJ
-__global__ void __launch_bounds__(kThreads) select_kernel(thin_attn_paged_attention_args a, int32_t* ids, int32_t* keys,
+__global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(thin_attn_paged_attention_args a, int32_t* ids, int32_t* keys,
                                                           int per) {
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -102,9 +107,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(thin_attn_paged_attent
   uint32_t* words = (uint32_t*)smem;                    // [per]
   int8_t* qv = (int8_t*)(words + ((per + 3) & ~3));     // [rows][q_stride]
   float* scale = (float*)(qv + rows * q_stride(a.E));   // [rows]
-  __shared__ int hist[2][256];
+  __shared__ __align__(16) int hist[2][kBins];
   __shared__ int sums[kWarps][2];
-  __shared__ int digit_s, left_s, counts_s[2];
+  __shared__ uint32_t range_s[kWarps][2], range_all[2];
+  __shared__ int digit_s, left_s, whole_s, counts_s[2];
   // the attention may be launched now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int row, len, pages;
@@ -119,15 +125,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(thin_attn_paged_attent
   int32_t* places = a.pages_out ? a.pages_out + ((int64_t)n * a.H + h) * a.top : nullptr;
   const int j0 = min(pages, rank * per), count = min(pages, j0 + per) - j0;   // this CTA's pages
   const bool all = pages <= take;   // no choice to make
+  auto forced = [&](int i) { return j0 + i < a.first || j0 + i >= pages - a.last; };
 
   if (!all) {
     round_queries<T>(a, n, h, G, rows, qv, scale);
-    hist[0][tid] = hist[1][tid] = 0;
+    for (int i = tid; i < 2 * kBins; i += kThreads) hist[0][i] = 0;
     __syncthreads();
+    uint32_t smallest = 0xFFFFFFFFu, largest = 0;
     const int r = lane >> 2, c = lane & 3, chunks = a.E / 8;
+    int next = warp * kGroup + r < count ? table[j0 + warp * kGroup + r] : -1;
     for (int i0 = warp * kGroup; i0 < count; i0 += kWarps * kGroup) {
-      const int i = i0 + r;
-      const int id = i < count ? table[j0 + i] : -1;
+      const int id = next, i = i0 + kWarps * kGroup + r;
+      next = i < count ? table[j0 + i] : -1;   // a product ahead
       const bool held = id >= 0 && id < a.n_pages;
       const int64_t at = (int64_t)(held ? id : 0) * a.H + h;
       const uint4* src = (const uint4*)(a.bounds + at * 2 * a.E);
@@ -166,56 +175,104 @@ __global__ void __launch_bounds__(kThreads) select_kernel(thin_attn_paged_attent
       const float mx = __shfl_sync(0xffffffffu, px, (lane & 7) << 2);
       const int k = i0 + lane;
       if (lane < 8 && k < count) {
-        const int j = j0 + k;
-        const float score = mx > 0.f ? (lane & 1 ? mine1 : mine0) * mx : -INFINITY;   // a page outside the pool: last
-        words[k] = j < a.first || j >= pages - a.last ? 0xFFFFFFFFu : rank_of(score);
+        const uint32_t w = rank_of(mx > 0.f ? (lane & 1 ? mine1 : mine0) * mx : -INFINITY);   // a page outside the pool: last
+        words[k] = w;
+        if (!forced(k)) {
+          smallest = min(smallest, w);
+          largest = max(largest, w);
+        }
       }
     }
+    smallest = __reduce_min_sync(0xffffffffu, smallest);
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    if (lane == 0) {
+      range_s[warp][0] = smallest;
+      range_s[warp][1] = largest;
+    }
     __syncthreads();
+    if (tid < 2) {
+      uint32_t x = range_s[0][tid];
+      for (int k = 1; k < kWarps; ++k) x = tid ? max(x, range_s[k][1]) : min(x, range_s[k][0]);
+      range_all[tid] = x;
+    }
   }
 
-  uint32_t threshold = 0;
-  int left = take;   // how many of the pages on the threshold are taken
+  // taken: forced pages, words >= floor, and the first `left` of the words floor - 1
+  uint64_t floor = 0;
+  int left = 0;
   if (!all) {
-    for (int round = 0; round < 4; ++round) {
-      const int shift = 24 - 8 * round;
+    cluster.sync();
+    uint32_t base = 0xFFFFFFFFu, top = 0;
+    for (int k = 0; k < ranks; ++k) {
+      const uint32_t* other = cluster.map_shared_rank(range_all, k);
+      base = min(base, other[0]);
+      top = max(top, other[1]);
+    }
+    left = take - a.first - a.last;
+    floor = (uint64_t)1 << 32;
+    uint32_t prefix = 0;
+    int shift = 32 - __clz(top - base);   // bits not yet decided
+    for (int round = 0; left > 0; ++round) {
+      const int bits = min(shift, 10), low = shift - bits;
       int* mine = hist[round & 1];
       for (int i = tid; i < count; i += kThreads) {
-        const uint32_t w = words[i];
-        if (round == 0 || (w ^ threshold) >> (shift + 8) == 0) atomicAdd(&mine[(w >> shift) & 255], 1);
+        const uint32_t w = words[i] - base;
+        if (!forced(i) && (shift >= 32 || w >> shift == prefix)) atomicAdd(&mine[(w >> low) & ((1 << bits) - 1)], 1);
       }
       cluster.sync();
-      // thread t: bin 255 - t of all CTAs; the bin at which the running count reaches `left`
-      int bin = 0;
-      for (int k = 0; k < ranks; ++k) bin += cluster.map_shared_rank(mine, k)[255 - tid];
-      int incl = bin;
+      // thread t: bins 1023 - 4 t and the three below, of all CTAs; the bin at which the running count reaches `left`
+      int bin[4] = {0, 0, 0, 0};
+      for (int k = 0; k < ranks; ++k) {
+        const int4 v = ((const int4*)cluster.map_shared_rank(mine, k))[kBins / 4 - 1 - tid];
+        bin[0] += v.w;
+        bin[1] += v.z;
+        bin[2] += v.y;
+        bin[3] += v.x;
+      }
+      int incl = (bin[0] + bin[1]) + (bin[2] + bin[3]);
+      int at = -incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
       if (lane == 31) sums[warp][0] = incl;
-      hist[(round & 1) ^ 1][tid] = 0;   // the other CTAs read it a round ago
+      ((int4*)hist[(round & 1) ^ 1])[tid] = make_int4(0, 0, 0, 0);   // the other CTAs read it a round ago
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < kWarps; ++k)
         if (k < warp) incl += sums[k][0];
-      if (incl - bin < left && incl >= left) {
-        digit_s = 255 - tid;
-        left_s = left - (incl - bin);
+      at += incl;   // in the bins above thread t's
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (at < left && at + bin[k] >= left) {
+          digit_s = kBins - 1 - 4 * tid - k;
+          left_s = left - at;
+          whole_s = at + bin[k] == left;
+        }
+        at += bin[k];
       }
       __syncthreads();
-      threshold |= (uint32_t)digit_s << shift;
+      prefix = prefix << bits | (uint32_t)digit_s;
       left = left_s;
+      shift = low;
+      if (whole_s) {          // the bin is taken whole
+        floor = (uint64_t)base + ((uint64_t)prefix << low);
+        left = 0;
+      } else if (low == 0) {
+        floor = (uint64_t)base + prefix + 1;
+        break;
+      }
     }
   }
-  // how many pages of this CTA lie above the threshold and on it
+  // how many of this CTA's pages are above, and how many on the word below
   int above = 0, on = 0;
   for (int i0 = 0; i0 < count; i0 += kThreads) {
-    const bool in = i0 + tid < count;
-    const uint32_t w = in && !all ? words[i0 + tid] : 0;
-    above += __syncthreads_count(in && (all || w > threshold));
-    on += __syncthreads_count(in && !all && w == threshold);
+    const int i = i0 + tid;
+    const bool in = i < count;
+    const uint64_t w = in && !all ? words[i] : 0;
+    above += __syncthreads_count(in && (all || forced(i) || w >= floor));
+    on += __syncthreads_count(in && !all && left && !forced(i) && w + 1 == floor);
   }
   if (tid == 0) {
     counts_s[0] = above;
@@ -228,13 +285,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(thin_attn_paged_attent
     before_above += other[0];
     before_on += other[1];
   }
-  if (all) left = 0;
   int placed = before_above + min(before_on, left);   // taken before this CTA's pages
   on = before_on;
   for (int i0 = 0; i0 < count; i0 += kThreads) {
     const int i = i0 + tid;
-    const uint32_t w = i < count && !all ? words[i] : 0;
-    const bool top = i < count && (all || w > threshold), equal = i < count && !all && w == threshold;
+    const uint64_t w = i < count && !all ? words[i] : 0;
+    const bool top = i < count && (all || forced(i) || w >= floor);
+    const bool equal = i < count && !all && left && !forced(i) && w + 1 == floor;
     const uint32_t eb = __ballot_sync(0xffffffffu, equal);
     if (lane == 0) sums[warp][0] = __popc(eb);
     __syncthreads();
@@ -267,9 +324,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(thin_attn_paged_attent
 template <typename T, int KJ>
 cudaError_t launch_t(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, cudaStream_t st) {
   const int rows = (a.Hq / a.H + 15) & ~15;
-  // one CTA per 64 pages that the table can hold, as far as a cluster reaches
+  // one CTA per 64 pages that the table can hold, as far as a cluster reaches, but no more CTAs than run
+  // at once (four per SM), unless the scores need the room
   int cluster = 1;
-  while (cluster < kMaxCluster && cluster * 64 < a.W) cluster *= 2;
+  while (cluster < kMaxCluster && cluster * 64 < a.W &&
+         ((int64_t)2 * cluster * a.N * a.H <= 148 * kPerSm || cluster * kMostPages < a.W))
+    cluster *= 2;
   const int per = (a.W + cluster - 1) / cluster;
   const size_t smem = (size_t)((per + 3) & ~3) * 4 + (size_t)rows * q_stride(a.E) + rows * 4;
   auto kernel = select_kernel<T, KJ>;
