@@ -31,7 +31,8 @@ cudaError_t launch_paged_attention(const PagedAttn& p, void* workspace, cudaStre
 
 // Page selection: per token and key head the chosen pages' ids (lists of `top`), and per token the
 // keys they hold.
-bool paged_select_fits(const thin_attn_paged_attention_args& a);   // scores and queries in shared memory
-cudaError_t launch_paged_select(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, cudaStream_t st);
+size_t paged_select_workspace(const thin_attn_paged_attention_args& a);
+cudaError_t launch_paged_select(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, void* workspace,
+                                cudaStream_t st);
 
 }  // namespace thin

@@ -71,14 +71,14 @@ thin_attn_status check_attention(const thin_attn_paged_attention_args* a) {
       return err(THIN_ATTN_EINVAL, "first=%d last=%d top=%d: need first >= 0, last >= 1, first + last <= top", a->first,
                  a->last, a->top);
     if (a->N > 65535 || a->H > 65535) return err(THIN_ATTN_EUNSUPPORTED, "page selection of %d tokens, %d heads: at most 65535", a->N, a->H);
-    if (!paged_select_fits(*a))
-      return err(THIN_ATTN_EUNSUPPORTED, "page selection over W=%d pages with %d queries per head: the scores outgrow shared memory", a->W, a->Hq / a->H);
+    if ((int64_t)a->N * a->H * a->W > kIntMax) return err(THIN_ATTN_EUNSUPPORTED, "page selection over N * H * W = %lld pages", (long long)a->N * a->H * a->W);
+    if (a->Hq / a->H > 256) return err(THIN_ATTN_EUNSUPPORTED, "page selection with %d queries per key head: at most 256", a->Hq / a->H);
   }
   return THIN_ATTN_OK;
 }
 
 struct Layout {
-  size_t ids, keys, attn, bytes;
+  size_t ids, keys, words, attn, bytes;
 };
 Layout layout_of(const thin_attn_paged_attention_args& a) {
   Layout l{};
@@ -88,6 +88,8 @@ Layout layout_of(const thin_attn_paged_attention_args& a) {
     at += al256((size_t)a.N * a.H * a.top * 4);
     l.keys = at;
     at += al256((size_t)a.N * 4);
+    l.words = at;
+    at += al256(paged_select_workspace(a));
   }
   l.attn = at;
   l.bytes = at + al256(paged_attention_workspace(a));
@@ -200,7 +202,7 @@ thin_attn_status thin_attn_paged_attention(const thin_attn_paged_attention_args*
   if (a->top) {
     int32_t* ids = (int32_t*)(ws + l.ids);
     int32_t* keys = (int32_t*)(ws + l.keys);
-    s = launched(launch_paged_select(*a, ids, keys, st), "page selection");
+    s = launched(launch_paged_select(*a, ids, keys, ws + l.words, st), "page selection");
     if (s != THIN_ATTN_OK) return s;
     p.ids = ids;
     p.ids_token = (int64_t)a->H * a->top;

@@ -1,9 +1,11 @@
 // New keys and values into their slots, with the bounds of every touched page's keys.
 //
-// A warp takes one run of neighbouring tokens that share a page (a single token without bounds), for
-// one key head: it copies the rows (rounding to e4m3 where the cache holds that) and keeps the
-// channels' running minimum and maximum, so the keys are read once.  Lane l holds channels 8 l ..
-// 8 l + 7 of a key row (E <= 256).  The exponent x is monotone in max |k|, and
+// A CTA takes a block of tokens of one key head (heads vary fastest, so that the rows of a token are
+// read together) and copies their rows in 16-byte pieces, rounded to e4m3 where the cache holds that.
+// It brings the bounds up to date for every run of neighbouring tokens that share a page and begins
+// in the block, to the run's end: runs of up to 16 tokens by one warp each, from L1; of longer ones every
+// thread takes the minimum and maximum of the pieces that it copies (and of some of the run's tokens
+// behind the block), and a warp per run joins them.  The exponent x is monotone in max |k|, and
 // floor(floor(u) / 2^s) = floor(u / 2^s), so widening stored bounds step by step gives the bounds
 // that all of the page's keys together would.  HBM bound: each row is read and written once.
 #include <cuda_bf16.h>
@@ -17,122 +19,322 @@ namespace thin {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMany = 64, kFew = 8;   // tokens of a block, at most
+constexpr int kPieces = 4;            // pieces of keys that a thread copies
+constexpr int kShort = 16;            // tokens of a run that one warp takes
 
+// Eight elements of type T as a cache of type C holds them; e4m3: the quotient is rounded to fp32, then to e4m3.
+template <typename C>
+struct Held {
+  static constexpr int kWords = 2 * (int)sizeof(C);
+  uint32_t w[kWords];
+};
 template <typename T, typename C>
-__device__ __forceinline__ void hold(const float (&x)[8], float scale, C* dst, float (&held)[8]) {
+__device__ __forceinline__ Held<C> held_of(const T* src, float scale) {
+  Held<C> y;
   if constexpr (sizeof(C) == 1) {
-    uint32_t w[2] = {0, 0};
+    float x[8];
+    load8(src, x);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i] / scale, x[i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i + 2] / scale, x[i + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+      y.w[i / 4] = lo | hi << 16;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < Held<C>::kWords; i += 4) {
+      const uint4 u = ((const uint4*)src)[i / 4];
+      y.w[i] = u.x;
+      y.w[i + 1] = u.y;
+      y.w[i + 2] = u.z;
+      y.w[i + 3] = u.w;
+    }
+  }
+  return y;
+}
+template <typename C>
+__device__ __forceinline__ void put_held(C* dst, const Held<C>& y) {
+  if constexpr (sizeof(C) == 1) {
+    *(uint2*)dst = make_uint2(y.w[0], y.w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Held<C>::kWords; i += 4) ((uint4*)dst)[i / 4] = make_uint4(y.w[i], y.w[i + 1], y.w[i + 2], y.w[i + 3]);
+  }
+}
+// Their values, a NaN as 0.
+template <typename C>
+__device__ __forceinline__ void values_of(const Held<C>& y, float (&x)[8]) {
+  if constexpr (sizeof(C) == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y.w[i / 4] >> (8 * (i & 3))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      x[i] = f.x;
+      x[i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = elem_f<C>(((const C*)y.w)[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] : 0.f;
+}
+
+// Minimum and maximum of a lane's 8 channels.
+struct Range {
+  float lo[8], hi[8];
+  __device__ __forceinline__ Range() {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // the quotient is rounded to fp32, then to e4m3
-      const uint32_t b = __nv_cvt_float_to_fp8(x[i] / scale, __NV_SATFINITE, __NV_E4M3);
-      w[i >> 2] |= b << (8 * (i & 3));
-      held[i] = e4m3_to_f(b);
+      lo[i] = INFINITY;
+      hi[i] = -INFINITY;
     }
-    *(uint2*)dst = make_uint2(w[0], w[1]);
-  } else {
-    store8(dst, x);
+  }
+  __device__ __forceinline__ void take(const float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) held[i] = x[i];
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = fminf(lo[i], x[i]);
+      hi[i] = fmaxf(hi[i], x[i]);
+    }
+  }
+  // with lanes l and l + per, l + 2 per ...
+  __device__ __forceinline__ void join(int per) {
+    for (int o = per; o < 32; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      }
+    }
+  }
+};
+// Over tokens first, first + step, ... below last.
+template <typename T, typename C>
+__device__ __forceinline__ void range_of(const thin_attn_paged_append_args& a, Range& g, int first, int last, int step, int h, int col, float ks) {
+  const T* src = (const T*)a.k + h * a.k_head + col;
+#pragma unroll 4
+  for (int t = first; t < last; t += step) {
+    float x[8];
+    values_of(held_of<T, C>(src + t * a.k_token, ks), x);
+    g.take(x);
   }
 }
 
-template <typename T, typename C>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(thin_attn_paged_append_args a) {
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (unit >= (int64_t)a.N * a.H) return;
-  const int first = (int)(unit / a.H), h = (int)(unit % a.H);
-  const int64_t slots = (int64_t)a.n_pages * a.page;
-  int64_t slot = a.slots[first];
-  if (slot < 0 || slot >= slots) return;
-  const int64_t pg = slot / a.page;
-  if (a.bounds && first > 0) {
-    const int64_t before = a.slots[first - 1];
-    if (before >= 0 && before < slots && before / a.page == pg) return;   // inside an earlier token's run
-  }
-  const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
-  float lo[8], hi[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
-  }
-  bool anew = false;
-  for (int t = first;;) {
-    const int64_t off = slot - pg * a.page;
-    anew |= off == 0;
-    if (lane * 8 < a.E) {
-      float x[8], held[8];
-      load8((const T*)a.k + t * a.k_token + h * a.k_head + lane * 8, x);
-      hold<T>(x, ks, (C*)a.k_pages + pg * a.kp_page + h * a.kp_head + off * a.kp_row + lane * 8, held);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = held[i] == held[i] ? held[i] : 0.f;
-        lo[i] = fminf(lo[i], y);
-        hi[i] = fmaxf(hi[i], y);
-      }
-    }
-    if (lane * 8 < a.D) {
-      float x[8], held[8];
-      load8((const T*)a.v + t * a.v_token + h * a.v_head + lane * 8, x);
-      hold<T>(x, vs, (C*)a.v_pages + pg * a.vp_page + h * a.vp_head + off * a.vp_row + lane * 8, held);
-    }
-    if (!a.bounds || ++t >= a.N) break;
-    slot = a.slots[t];
-    if (slot < pg * a.page || slot >= (pg + 1) * a.page) break;
-  }
-  if (!a.bounds) return;
+struct Stored {
+  uint2 lo, hi;
+  int exp;
+};
+
+// A warp writes the bounds of one page and head: of `g` alone, or the stored ones widened.  Lanes of the same
+// channels hold the same range.
+__device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& a, const Range& g, const Stored& old, bool anew,
+                                             int64_t at, int col, bool writes, int lane) {
   float m = 0.f;
-  const bool mine = lane * 8 < a.E;
-  if (mine) {
+  if (col < a.E) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(g.lo[i]), fabsf(g.hi[i])));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  int x = bound_exponent(m);
-  int8_t* row = a.bounds + (pg * a.H + h) * 2 * a.E;
-  int8_t* exp = a.exps + pg * a.H + h;
-  const int x0 = anew ? x : *exp;
-  const int up = max(0, x - x0);   // the stored bounds' steps grow by 2^up
-  x = max(x, x0);
-  __syncwarp();                    // every lane has read the exponent
-  if (lane == 0) *exp = (int8_t)x;
-  if (!mine) return;
+  const int x1 = bound_exponent(m), x = anew ? x1 : max(x1, old.exp);
+  const int up = min(anew ? 0 : x - old.exp, 31);   // the stored bounds' steps grow by 2^up
+  if (lane == 0) a.exps[at] = (int8_t)x;
+  if (!writes || col >= a.E) return;
   const float inv = pow2f(-x);
-  uint2 wl = make_uint2(0, 0), wh = wl, ol = wl, oh = wl;
-  if (!anew) {
-    ol = *(const uint2*)(row + lane * 8);
-    oh = *(const uint2*)(row + a.E + lane * 8);
-  }
+  uint32_t wl[2] = {0, 0}, wh[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int l = (int)fminf(fmaxf(floorf(lo[i] * inv), -127.f), 127.f);
-    int u = (int)fminf(fmaxf(ceilf(hi[i] * inv), -127.f), 127.f);
+    int l = (int)fminf(fmaxf(floorf(g.lo[i] * inv), -127.f), 127.f);
+    int u = (int)fminf(fmaxf(ceilf(g.hi[i] * inv), -127.f), 127.f);
     if (!anew) {
-      const int sl = (int8_t)((i < 4 ? ol.x : ol.y) >> (8 * (i & 3))), sh = (int8_t)((i < 4 ? oh.x : oh.y) >> (8 * (i & 3)));
-      l = min(l, sl >> min(up, 31));
-      u = max(u, -((-sh) >> min(up, 31)));
+      const int sl = (int8_t)((i < 4 ? old.lo.x : old.lo.y) >> (8 * (i & 3))), sh = (int8_t)((i < 4 ? old.hi.x : old.hi.y) >> (8 * (i & 3)));
+      l = min(l, sl >> up);
+      u = max(u, -((-sh) >> up));
     }
-    const uint32_t bl = (uint32_t)(l & 0xFF) << (8 * (i & 3)), bu = (uint32_t)(u & 0xFF) << (8 * (i & 3));
-    if (i < 4) {
-      wl.x |= bl;
-      wh.x |= bu;
-    } else {
-      wl.y |= bl;
-      wh.y |= bu;
+    wl[i >> 2] |= (uint32_t)(l & 0xFF) << (8 * (i & 3));
+    wh[i >> 2] |= (uint32_t)(u & 0xFF) << (8 * (i & 3));
+  }
+  int8_t* row = a.bounds + at * 2 * a.E;
+  *(uint2*)(row + col) = make_uint2(wl[0], wl[1]);
+  *(uint2*)(row + a.E + col) = make_uint2(wh[0], wh[1]);
+}
+
+template <typename T, typename C>
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(thin_attn_paged_append_args a, int block, int k_shift, int v_shift) {
+  // k_shift, v_shift: 2^shift threads take a row, 8 elements each
+  const int h = blockIdx.x % a.H, t0 = blockIdx.x / a.H * block, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int page_s[kMany + 2], off_s[kMany];   // page_s[0]: the token before the block, [block + 1]: none
+  if (tid <= block + 1) {
+    const int t = t0 + tid - 1;
+    const int64_t slot = t >= 0 && t < a.N && tid <= block ? a.slots[t] : -1;
+    int pg = -1;
+    if (slot >= 0 && slot < (int64_t)a.n_pages * a.page) {
+      pg = slot >> 32 ? (int)(slot / a.page) : (int)((uint32_t)slot / (uint32_t)a.page);
+      if (tid > 0) off_s[tid - 1] = (int)(slot - (int64_t)pg * a.page);
+    }
+    page_s[tid] = pg;
+  }
+  __syncthreads();
+  const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
+  const int k_col = (tid & ((1 << k_shift) - 1)) * 8, v_col = (tid & ((1 << v_shift) - 1)) * 8;
+  const int k_row = tid >> k_shift, v_row = tid >> v_shift, k_step = kThreads >> k_shift, v_step = kThreads >> v_shift;
+  Held<C> x[kPieces];
+  // the host chose the block so that kPieces turns cover its keys
+  bool has[kPieces];
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int r = k_row + u * k_step;
+    has[u] = r < block && k_col < a.E && page_s[r + 1] >= 0;
+    if (has[u]) x[u] = held_of<T, C>((const T*)a.k + (t0 + r) * a.k_token + h * a.k_head + k_col, ks);
+  }
+  for (int r0 = v_row; r0 < block; r0 += kPieces * v_step) {
+    Held<C> y[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int r = r0 + u * v_step;
+      if (r < block && v_col < a.D && page_s[r + 1] >= 0) y[u] = held_of<T, C>((const T*)a.v + (t0 + r) * a.v_token + h * a.v_head + v_col, vs);
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int r = r0 + u * v_step;
+      if (r < block && v_col < a.D && page_s[r + 1] >= 0)
+        put_held((C*)a.v_pages + page_s[r + 1] * a.vp_page + h * a.vp_head + off_s[r] * a.vp_row + v_col, y[u]);
     }
   }
-  *(uint2*)(row + lane * 8) = wl;
-  *(uint2*)(row + a.E + lane * 8) = wh;
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int r = k_row + u * k_step;
+    if (has[u]) put_held((C*)a.k_pages + page_s[r + 1] * a.kp_page + h * a.kp_head + off_s[r] * a.kp_row + k_col, x[u]);
+  }
+  if (!a.bounds) return;
+
+  // tokens behind the block that go on with its last run, and whether one of them is its page's first slot
+  int tail = 0;
+  bool tail_anew = false;
+  if (page_s[block] >= 0) {
+    const int64_t begin = (int64_t)page_s[block] * a.page;
+    for (;; tail += 32) {
+      const int t = t0 + block + tail + lane;
+      const int64_t slot = t < a.N ? a.slots[t] : -1;
+      const uint32_t in = __ballot_sync(0xffffffffu, slot >= begin && slot < begin + a.page);
+      const int run = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+      tail_anew |= __any_sync(0xffffffffu, lane < run && slot == begin);
+      if (run < 32) {
+        tail += run;
+        break;
+      }
+    }
+  }
+  // at most kMany / kShort runs of more than kShort tokens begin in a block; twice 256 floats for two of
+  // them where rows are wide, for four otherwise
+  __shared__ __align__(16) float part[kWarps * 2 * 512];
+  const int per = 1 << k_shift, col = (lane & (per - 1)) * 8, sub = lane >> k_shift, rows = 32 >> k_shift;
+  int shorts = 0, longs = 0;
+  // bit i: token i begins a run, or goes to its page's first slot
+  uint64_t starts = 0, fresh = 0;
+#pragma unroll
+  for (int x2 = 0; x2 < kMany; x2 += 32) {
+    const int i = x2 + lane;
+    starts |= (uint64_t)__ballot_sync(0xffffffffu, i < block && (i == 0 || page_s[i + 1] != page_s[i])) << x2;
+    fresh |= (uint64_t)__ballot_sync(0xffffffffu, i < block && page_s[i + 1] >= 0 && off_s[i] == 0) << x2;
+  }
+  // every run that begins in the block: its first token, its tokens, its page, whether it starts the page anew
+  auto runs = [&](auto&& f) {
+    for (uint64_t left = starts; left;) {
+      const int begin = __ffsll(left) - 1;
+      left &= left - 1;
+      const int end = left ? __ffsll(left) - 1 : block, pg = page_s[begin + 1];
+      if (pg < 0 || pg == page_s[begin]) continue;   // no token, or the rest of a run that began before the block
+      const bool anew = (fresh >> begin & (~0ull >> (64 - (end - begin)))) || (end == block && tail_anew);
+      f(begin, end - begin + (end == block ? tail : 0), pg, anew);
+    }
+  };
+  auto stored = [&](int64_t at, bool anew) {
+    Stored old{};
+    if (!anew) {
+      if (col < a.E) {
+        old.lo = *(const uint2*)(a.bounds + at * 2 * a.E + col);
+        old.hi = *(const uint2*)(a.bounds + at * 2 * a.E + a.E + col);
+      }
+      old.exp = a.exps[at];
+      __syncwarp();   // before lane 0 writes the exponent
+    }
+    return old;
+  };
+  runs([&](int begin, int n, int pg, bool anew) {
+    if (n <= kShort) {
+      if (shorts++ % kWarps != warp) return;
+      const int64_t at = (int64_t)pg * a.H + h;
+      const Stored old = stored(at, anew);
+      Range g;
+      if (col < a.E) range_of<T, C>(a, g, t0 + begin + sub, t0 + begin + n, rows, h, col, ks);
+      g.join(per);
+      write_bounds(a, g, old, anew, at, col, sub == 0, lane);
+      return;
+    }
+    Range g;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int r = k_row + u * k_step;
+      if (!has[u] || r < begin || r >= begin + n) continue;
+      float f[8];
+      values_of(x[u], f);
+      g.take(f);
+    }
+    if (begin + n > block && col < a.E)
+      range_of<T, C>(a, g, t0 + block + warp * rows + sub, t0 + begin + n, kWarps * rows, h, col, ks);
+    g.join(per);
+    if (sub == 0 && col < a.E) {
+      float* dst = part + (longs * kWarps + warp) * 2 * a.E + col;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dst[k] = g.lo[k];
+        dst[a.E + k] = g.hi[k];
+      }
+    }
+    ++longs;
+  });
+  if (longs == 0) return;   // for every thread of the CTA alike
+  __syncthreads();
+  longs = 0;
+  runs([&](int begin, int n, int pg, bool anew) {
+    if (n <= kShort || longs++ % kWarps != warp) return;
+    const int64_t at = (int64_t)pg * a.H + h;
+    const Stored old = stored(at, anew);
+    Range g;
+    if (col < a.E) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* src = part + ((longs - 1) * kWarps + w) * 2 * a.E + col;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          g.lo[k] = fminf(g.lo[k], src[k]);
+          g.hi[k] = fmaxf(g.hi[k], src[a.E + k]);
+        }
+      }
+    }
+    write_bounds(a, g, old, anew, at, col, sub == 0, lane);
+  });
+}
+
+int shift_of(int width) {
+  int s = 0;
+  while ((8 << s) < width) ++s;
+  return s;
 }
 
 template <typename T, typename C>
 cudaError_t launch_t(const thin_attn_paged_append_args& a, cudaStream_t st) {
-  const int64_t units = (int64_t)a.N * a.H;
-  append_kernel<T, C><<<(unsigned)((units + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a);
+  const int k_shift = shift_of(a.E), v_shift = shift_of(a.D);
+  // as many tokens as kPieces turns cover, where such blocks fill the GPU; few for a decode step's
+  // tokens, one page each
+  int block = kPieces * kThreads >> k_shift;
+  if (block > kMany) block = kMany;
+  if ((int64_t)a.N * a.H < 148 * kMany) block = kFew;
+  const int64_t grid = (int64_t)((a.N + block - 1) / block) * a.H;
+  append_kernel<T, C><<<(unsigned)grid, kThreads, 0, st>>>(a, block, k_shift, v_shift);
   return cudaGetLastError();
 }
 

@@ -10,30 +10,23 @@
 // of the summed index is free, so a lane takes its fragments as 16-byte pieces of a page's 2 E
 // bytes, straight from global memory; each is read once.
 //
-// A cluster of CTAs serves one (token, key head), each an equal run of its pages, the scores in shared
-// memory as words of the same order.  The smallest word taken is found by a radix search, 10 bits a
-// round from the leading bit of (largest - smallest word), with histograms that the CTAs read from
-// one another; it ends as soon as a bin is taken whole, mostly in the second round.  Then each CTA writes
-// its pages above that word, and the first of those on it, behind the pages of the CTAs before it, so
-// the lists ascend.
-#include <cooperative_groups.h>
-
+// score_kernel: CTAs take equal runs of the pages of one (token, key head) and write the scores as words
+// of the same order.  select_kernel: one CTA per (token, key head) finds the smallest word
+// taken by a radix search, 10 bits a round from the leading bit of (largest - smallest word); it ends as
+// soon as a bin is taken whole, mostly in the second round.  Then it writes the pages above that
+// word, and the first of those on it, in ascending order.
 #include "paged.h"
 #include "paged_types.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace thin {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kPerSm = 4;
-constexpr int kMostPages = 4096;   // of a CTA, where a larger cluster can be had
-constexpr int kGroup = 8;   // pages of one product
-constexpr int kBins = 1024;
+constexpr int kWarps = 8;          // of a scoring CTA
+constexpr int kGroup = 8;          // pages of one product
+constexpr int kSelectThreads = 512;
+constexpr int kBins = 1024, kOwn = kBins / kSelectThreads;   // a thread adds up kOwn bins
+constexpr int kHeld = 8192;        // words that the selection keeps in shared memory; more are read again
 
 // Token n's request and the pages its keys reach; false for padding.
 __device__ __forceinline__ bool token_pages(const thin_attn_paged_attention_args& a, int n, int* row, int* len, int* pages) {
@@ -96,54 +89,48 @@ __device__ __forceinline__ void round_queries(const thin_attn_paged_attention_ar
   }
 }
 
+// A page outside the pool scores lowest.
 template <typename T, int KJ>   // KJ: 16-byte pieces per lane and page, 2 E <= 64 KJ
-__global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(thin_attn_paged_attention_args a, int32_t* ids, int32_t* keys,
-                                                          int per) {
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int n = blockIdx.z, h = blockIdx.y, G = a.Hq / a.H, rows = (G + 15) & ~15;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  extern __shared__ __align__(16) unsigned char smem[];
-  uint32_t* words = (uint32_t*)smem;                    // [per]
-  int8_t* qv = (int8_t*)(words + ((per + 3) & ~3));     // [rows][q_stride]
-  float* scale = (float*)(qv + rows * q_stride(a.E));   // [rows]
-  __shared__ __align__(16) int hist[2][kBins];
-  __shared__ int sums[kWarps][2];
-  __shared__ uint32_t range_s[kWarps][2], range_all[2];
-  __shared__ int digit_s, left_s, whole_s, counts_s[2];
-  // the attention may be launched now; it waits for this grid's end before it reads
+__global__ void __launch_bounds__(kWarps * 32) score_kernel(thin_attn_paged_attention_args a, uint32_t* words, int per) {
+  // the selection may be launched now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n = blockIdx.z, h = blockIdx.y, G = a.Hq / a.H, rows = (G + 15) & ~15;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ __align__(16) unsigned char smem[];
+  int8_t* qv = (int8_t*)smem;                           // [rows][q_stride]
+  float* scale = (float*)(qv + rows * q_stride(a.E));   // [rows]
   int row, len, pages;
-  if (!token_pages(a, n, &row, &len, &pages)) {   // the whole cluster returns
-    if (tid == 0 && h == 0 && rank == 0) keys[n] = 0;
-    return;
-  }
-  const int take = min(a.top, pages);
-  if (tid == 0 && h == 0 && rank == 0) keys[n] = take ? (take - 1) * a.page + len - (pages - 1) * a.page : 0;
-  const int32_t* table = a.table + row * a.table_row;
-  int32_t* list = ids + ((int64_t)n * a.H + h) * a.top;
-  int32_t* places = a.pages_out ? a.pages_out + ((int64_t)n * a.H + h) * a.top : nullptr;
-  const int j0 = min(pages, rank * per), count = min(pages, j0 + per) - j0;   // this CTA's pages
-  const bool all = pages <= take;   // no choice to make
-  auto forced = [&](int i) { return j0 + i < a.first || j0 + i >= pages - a.last; };
-
-  if (!all) {
-    round_queries<T>(a, n, h, G, rows, qv, scale);
-    for (int i = tid; i < 2 * kBins; i += kThreads) hist[0][i] = 0;
-    __syncthreads();
-    uint32_t smallest = 0xFFFFFFFFu, largest = 0;
-    const int r = lane >> 2, c = lane & 3, chunks = a.E / 8;
-    int next = warp * kGroup + r < count ? table[j0 + warp * kGroup + r] : -1;
-    for (int i0 = warp * kGroup; i0 < count; i0 += kWarps * kGroup) {
-      const int id = next, i = i0 + kWarps * kGroup + r;
-      next = i < count ? table[j0 + i] : -1;   // a product ahead
-      const bool held = id >= 0 && id < a.n_pages;
-      const int64_t at = (int64_t)(held ? id : 0) * a.H + h;
-      const uint4* src = (const uint4*)(a.bounds + at * 2 * a.E);
-      uint4 b[KJ];
+  if (!token_pages(a, n, &row, &len, &pages) || pages <= a.top) return;   // no choice to make
+  const int j0 = blockIdx.x * per, count = min(pages - j0, per);
+  if (count <= 0) return;
+  const int32_t* table = a.table + row * a.table_row + j0;
+  words += ((int64_t)n * a.H + h) * a.W + j0;
+  const int r = lane >> 2, c = lane & 3, chunks = a.E / 8;
+  // kAhead products' pages at a time, their ids fetched a turn before
+  constexpr int kAhead = KJ <= 4 ? 2 : 1, kTurn = kWarps * kGroup * kAhead;
+  int next[kAhead];
+  auto look = [&](int i0) {
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) b[j] = held && c + 4 * j < chunks ? src[c + 4 * j] : make_uint4(0, 0, 0, 0);
-      const float px = held ? pow2f(a.exps[at]) : 0.f;
+    for (int u = 0; u < kAhead; ++u) next[u] = i0 + u * kGroup + r < count ? table[i0 + u * kGroup + r] : -1;
+  };
+  look(warp * kGroup * kAhead);
+  round_queries<T>(a, n, h, G, rows, qv, scale);
+  __syncthreads();
+  for (int i0 = warp * kGroup * kAhead; i0 < count; i0 += kTurn) {
+    uint4 b[kAhead][KJ];
+    float px[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const bool held = next[u] >= 0 && next[u] < a.n_pages;
+      const int64_t at = (int64_t)(held ? next[u] : 0) * a.H + h;
+      const uint4* src = (const uint4*)(a.bounds + at * 2 * a.E);
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) b[u][j] = held && c + 4 * j < chunks ? src[c + 4 * j] : make_uint4(0, 0, 0, 0);
+      px[u] = held ? pow2f(a.exps[at]) : 0.f;
+    }
+    look(i0 + kTurn);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
       float best[2] = {-INFINITY, -INFINITY};   // of pages 2 c and 2 c + 1
       for (int m0 = 0; m0 < G; m0 += 16) {
         int s[4] = {0, 0, 0, 0};
@@ -155,8 +142,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(thin_attn_page
             if (m0 + 8 < G) q1 = *(const uint4*)(qv + (m0 + r + 8) * q_stride(a.E) + (c + 4 * j) * 16);
           }
           const uint32_t a0[4] = {q0.x, q1.x, q0.y, q1.y}, a1[4] = {q0.z, q1.z, q0.w, q1.w};
-          mma_s8(s, a0, b[j].x, b[j].y);
-          mma_s8(s, a1, b[j].z, b[j].w);
+          mma_s8(s, a0, b[u][j].x, b[u][j].y);
+          mma_s8(s, a1, b[u][j].z, b[u][j].w);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -171,201 +158,212 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(thin_attn_page
         best[1] = fmaxf(best[1], __shfl_xor_sync(0xffffffffu, best[1], o));
       }
       // lane 4 r' + c has page r' in `px` and pages 2 c, 2 c + 1 in `best`: lanes 0..7 take one page each
-      const float mine0 = __shfl_sync(0xffffffffu, best[0], (lane & 7) >> 1), mine1 = __shfl_sync(0xffffffffu, best[1], (lane & 7) >> 1);
-      const float mx = __shfl_sync(0xffffffffu, px, (lane & 7) << 2);
-      const int k = i0 + lane;
-      if (lane < 8 && k < count) {
-        const uint32_t w = rank_of(mx > 0.f ? (lane & 1 ? mine1 : mine0) * mx : -INFINITY);   // a page outside the pool: last
-        words[k] = w;
-        if (!forced(k)) {
-          smallest = min(smallest, w);
-          largest = max(largest, w);
-        }
-      }
-    }
-    smallest = __reduce_min_sync(0xffffffffu, smallest);
-    largest = __reduce_max_sync(0xffffffffu, largest);
-    if (lane == 0) {
-      range_s[warp][0] = smallest;
-      range_s[warp][1] = largest;
-    }
-    __syncthreads();
-    if (tid < 2) {
-      uint32_t x = range_s[0][tid];
-      for (int k = 1; k < kWarps; ++k) x = tid ? max(x, range_s[k][1]) : min(x, range_s[k][0]);
-      range_all[tid] = x;
+      const float b0 = __shfl_sync(0xffffffffu, best[0], (lane & 7) >> 1), b1 = __shfl_sync(0xffffffffu, best[1], (lane & 7) >> 1);
+      const float mx = __shfl_sync(0xffffffffu, px[u], (lane & 7) << 2);
+      const int k = i0 + u * kGroup + lane;
+      if (lane < 8 && k < count) words[k] = rank_of(mx > 0.f ? (lane & 1 ? b1 : b0) * mx : -INFINITY);
     }
   }
+}
+
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(thin_attn_paged_attention_args a, const uint32_t* words,
+                                                                 int32_t* ids, int32_t* keys) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kThreads = kSelectThreads, kSelectWarps = kThreads / 32;
+  const int n = blockIdx.y, h = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint32_t held[kHeld];
+  __shared__ int hist[2][kBins];
+  __shared__ int sums[kSelectWarps][2];
+  __shared__ uint32_t range[kSelectWarps][2];
+  __shared__ int digit_s, left_s, whole_s;
+  for (int i = tid; i < 2 * kBins; i += kThreads) hist[0][i] = 0;
+  int row, len, pages;
+  const bool live = token_pages(a, n, &row, &len, &pages);
+  // for the scores; every CTA waits, so that this grid's end means the scoring's end too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) {
+    if (tid == 0 && h == 0) keys[n] = 0;
+    return;
+  }
+  const int take = min(a.top, pages);
+  if (tid == 0 && h == 0) keys[n] = take ? (take - 1) * a.page + len - (pages - 1) * a.page : 0;
+  const int32_t* table = a.table + row * a.table_row;
+  int32_t* list = ids + ((int64_t)n * a.H + h) * a.top;
+  int32_t* places = a.pages_out ? a.pages_out + ((int64_t)n * a.H + h) * a.top : nullptr;
+  if (places)
+    for (int i = take + tid; i < a.top; i += kThreads) places[i] = -1;
+  if (pages <= take) {
+    for (int i = tid; i < take; i += kThreads) {
+      list[i] = table[i];
+      if (places) places[i] = i;
+    }
+    return;
+  }
+  words += ((int64_t)n * a.H + h) * a.W;
+  auto forced = [&](int i) { return i < a.first || i >= pages - a.last; };
+  uint32_t base = 0xFFFFFFFFu, most = 0;
+  for (int i = tid; i < pages; i += kThreads) {
+    const uint32_t w = words[i];
+    if (pages <= kHeld) held[i] = w;
+    if (!forced(i)) {
+      base = min(base, w);
+      most = max(most, w);
+    }
+  }
+  base = __reduce_min_sync(0xffffffffu, base);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    range[warp][0] = base;
+    range[warp][1] = most;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSelectWarps; ++k) {
+    base = min(base, range[k][0]);
+    most = max(most, range[k][1]);
+  }
+  const uint32_t* w_of = pages <= kHeld ? held : words;
 
   // taken: forced pages, words >= floor, and the first `left` of the words floor - 1
-  uint64_t floor = 0;
-  int left = 0;
-  if (!all) {
-    cluster.sync();
-    uint32_t base = 0xFFFFFFFFu, top = 0;
-    for (int k = 0; k < ranks; ++k) {
-      const uint32_t* other = cluster.map_shared_rank(range_all, k);
-      base = min(base, other[0]);
-      top = max(top, other[1]);
+  uint64_t floor = (uint64_t)1 << 32;
+  int left = take - a.first - a.last;
+  uint32_t prefix = 0;
+  int shift = 32 - __clz(most - base);   // bits not yet decided
+  for (int round = 0; left > 0; ++round) {
+    const int bits = min(shift, 10), low = shift - bits;
+    int* mine = hist[round & 1];
+    for (int i = tid; i < pages; i += kThreads) {
+      const uint32_t w = w_of[i] - base;
+      if (!forced(i) && (shift >= 32 || w >> shift == prefix)) atomicAdd(&mine[(w >> low) & ((1 << bits) - 1)], 1);
     }
-    left = take - a.first - a.last;
-    floor = (uint64_t)1 << 32;
-    uint32_t prefix = 0;
-    int shift = 32 - __clz(top - base);   // bits not yet decided
-    for (int round = 0; left > 0; ++round) {
-      const int bits = min(shift, 10), low = shift - bits;
-      int* mine = hist[round & 1];
-      for (int i = tid; i < count; i += kThreads) {
-        const uint32_t w = words[i] - base;
-        if (!forced(i) && (shift >= 32 || w >> shift == prefix)) atomicAdd(&mine[(w >> low) & ((1 << bits) - 1)], 1);
-      }
-      cluster.sync();
-      // thread t: bins 1023 - 4 t and the three below, of all CTAs; the bin at which the running count reaches `left`
-      int bin[4] = {0, 0, 0, 0};
-      for (int k = 0; k < ranks; ++k) {
-        const int4 v = ((const int4*)cluster.map_shared_rank(mine, k))[kBins / 4 - 1 - tid];
-        bin[0] += v.w;
-        bin[1] += v.z;
-        bin[2] += v.y;
-        bin[3] += v.x;
-      }
-      int incl = (bin[0] + bin[1]) + (bin[2] + bin[3]);
-      int at = -incl;
+    __syncthreads();
+    // thread t: its bins from the top down; the bin at which the running count reaches `left`
+    int bin[kOwn], incl = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) sums[warp][0] = incl;
-      ((int4*)hist[(round & 1) ^ 1])[tid] = make_int4(0, 0, 0, 0);   // the other CTAs read it a round ago
-      __syncthreads();
+    for (int x = 0; x < kOwn; ++x) {
+      bin[x] = mine[kBins - 1 - kOwn * tid - x];
+      incl += bin[x];
+      hist[(round & 1) ^ 1][x * kThreads + tid] = 0;
+    }
+    int at = -incl;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        if (k < warp) incl += sums[k][0];
-      at += incl;   // in the bins above thread t's
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[warp][0] = incl;
+    __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (at < left && at + bin[k] >= left) {
-          digit_s = kBins - 1 - 4 * tid - k;
-          left_s = left - at;
-          whole_s = at + bin[k] == left;
-        }
-        at += bin[k];
+    for (int k = 0; k < kSelectWarps; ++k)
+      if (k < warp) incl += sums[k][0];
+    at += incl;   // in the bins above thread t's
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      if (at < left && at + bin[k] >= left) {
+        digit_s = kBins - 1 - kOwn * tid - k;
+        left_s = left - at;
+        whole_s = at + bin[k] == left;
       }
-      __syncthreads();
-      prefix = prefix << bits | (uint32_t)digit_s;
-      left = left_s;
-      shift = low;
-      if (whole_s) {          // the bin is taken whole
-        floor = (uint64_t)base + ((uint64_t)prefix << low);
-        left = 0;
-      } else if (low == 0) {
-        floor = (uint64_t)base + prefix + 1;
-        break;
-      }
+      at += bin[k];
+    }
+    __syncthreads();
+    prefix = prefix << bits | (uint32_t)digit_s;
+    left = left_s;
+    shift = low;
+    if (whole_s) {          // the bin is taken whole
+      floor = (uint64_t)base + ((uint64_t)prefix << low);
+      left = 0;
+    } else if (low == 0) {
+      floor = (uint64_t)base + prefix + 1;
+      break;
     }
   }
-  // how many of this CTA's pages are above, and how many on the word below
+  // each warp takes a run of pages: how many are above, and how many on the word below
+  const int run = ((pages + kSelectWarps - 1) / kSelectWarps + 31) & ~31, from = min(pages, warp * run), to = min(pages, from + run);
+  auto look_at = [&](int i, bool* top, bool* equal) {
+    const uint64_t w = i < to ? w_of[i] : 0;
+    *top = i < to && (forced(i) || w >= floor);
+    *equal = i < to && !*top && left && w + 1 == floor;
+  };
   int above = 0, on = 0;
-  for (int i0 = 0; i0 < count; i0 += kThreads) {
-    const int i = i0 + tid;
-    const bool in = i < count;
-    const uint64_t w = in && !all ? words[i] : 0;
-    above += __syncthreads_count(in && (all || forced(i) || w >= floor));
-    on += __syncthreads_count(in && !all && left && !forced(i) && w + 1 == floor);
+  for (int i0 = from; i0 < to; i0 += 32) {
+    bool top, equal;
+    look_at(i0 + lane, &top, &equal);
+    above += __popc(__ballot_sync(0xffffffffu, top));
+    on += __popc(__ballot_sync(0xffffffffu, equal));
   }
-  if (tid == 0) {
-    counts_s[0] = above;
-    counts_s[1] = on;
+  __syncthreads();   // the sums of the last round have been read
+  if (lane == 0) {
+    sums[warp][0] = above;
+    sums[warp][1] = on;
   }
-  cluster.sync();
-  int before_above = 0, before_on = 0;
-  for (int k = 0; k < rank; ++k) {
-    const int* other = cluster.map_shared_rank(counts_s, k);
-    before_above += other[0];
-    before_on += other[1];
-  }
-  int placed = before_above + min(before_on, left);   // taken before this CTA's pages
-  on = before_on;
-  for (int i0 = 0; i0 < count; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint64_t w = i < count && !all ? words[i] : 0;
-    const bool top = i < count && (all || forced(i) || w >= floor);
-    const bool equal = i < count && !all && left && !forced(i) && w + 1 == floor;
-    const uint32_t eb = __ballot_sync(0xffffffffu, equal);
-    if (lane == 0) sums[warp][0] = __popc(eb);
-    __syncthreads();
-    int order = on + __popc(eb & ((1u << lane) - 1));
+  __syncthreads();
+  above = on = 0;   // in the pages before this warp's
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) order += sums[k][0];
-      on += sums[k][0];
+  for (int k = 0; k < kSelectWarps; ++k)
+    if (k < warp) {
+      above += sums[k][0];
+      on += sums[k][1];
     }
-    const bool got = top || (equal && order < left);
-    const uint32_t gb = __ballot_sync(0xffffffffu, got);
-    if (lane == 0) sums[warp][1] = __popc(gb);
-    __syncthreads();
-    int at = placed + __popc(gb & ((1u << lane) - 1));
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) at += sums[k][1];
-      placed += sums[k][1];
+  for (int i0 = from; i0 < to; i0 += 32) {
+    bool top, equal;
+    look_at(i0 + lane, &top, &equal);
+    const uint32_t tb = __ballot_sync(0xffffffffu, top), eb = __ballot_sync(0xffffffffu, equal), under = (1u << lane) - 1;
+    const int order = on + __popc(eb & under);
+    if (top || (equal && order < left)) {
+      const int at = above + __popc(tb & under) + min(order, left), j = i0 + lane;
+      list[at] = table[j];
+      if (places) places[at] = j;
     }
-    if (got) {
-      list[at] = table[j0 + i];
-      if (places) places[at] = j0 + i;
-    }
+    above += __popc(tb);
+    on += __popc(eb);
   }
-  if (places && rank == 0)
-    for (int i = take + tid; i < a.top; i += kThreads) places[i] = -1;
-  cluster.sync();   // no CTA ends while another reads its counts
 }
 
 template <typename T, int KJ>
-cudaError_t launch_t(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, cudaStream_t st) {
+cudaError_t score_t(const thin_attn_paged_attention_args& a, uint32_t* words, cudaStream_t st) {
   const int rows = (a.Hq / a.H + 15) & ~15;
-  // one CTA per 64 pages that the table can hold, as far as a cluster reaches, but no more CTAs than run
-  // at once (four per SM), unless the scores need the room
-  int cluster = 1;
-  while (cluster < kMaxCluster && cluster * 64 < a.W &&
-         ((int64_t)2 * cluster * a.N * a.H <= 148 * kPerSm || cluster * kMostPages < a.W))
-    cluster *= 2;
-  const int per = (a.W + cluster - 1) / cluster;
-  const size_t smem = (size_t)((per + 3) & ~3) * 4 + (size_t)rows * q_stride(a.E) + rows * 4;
-  auto kernel = select_kernel<T, KJ>;
+  // 128 pages per CTA, one turn, while those CTAs run at once (four per SM); four turns where there are more
+  int per = 128;
+  if ((int64_t)((a.W + per - 1) / per) * a.N * a.H > 148 * 4) per = 512;
+  const size_t smem = (size_t)rows * q_stride(a.E) + rows * 4;
+  auto kernel = score_kernel<T, KJ>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(cluster, a.H, a.N);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, ids, keys, per);
+  kernel<<<dim3((a.W + per - 1) / per, a.H, a.N), kWarps * 32, smem, st>>>(a, words, per);
+  return cudaGetLastError();
 }
 template <typename T>
-cudaError_t launch_e(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, cudaStream_t st) {
-  if (a.E <= 64) return launch_t<T, 2>(a, ids, keys, st);
-  if (a.E <= 128) return launch_t<T, 4>(a, ids, keys, st);
-  return launch_t<T, 8>(a, ids, keys, st);
+cudaError_t score_e(const thin_attn_paged_attention_args& a, uint32_t* words, cudaStream_t st) {
+  if (a.E <= 64) return score_t<T, 2>(a, words, st);
+  if (a.E <= 128) return score_t<T, 4>(a, words, st);
+  return score_t<T, 8>(a, words, st);
 }
 
 }  // namespace
 
-bool paged_select_fits(const thin_attn_paged_attention_args& a) {
-  const int64_t rows = (a.Hq / a.H + 15) & ~15, per = ((int64_t)a.W + kMaxCluster - 1) / kMaxCluster;
-  return per * 4 + 16 + rows * (q_stride(a.E) + 4) <= 224 * 1024;
-}
+size_t paged_select_workspace(const thin_attn_paged_attention_args& a) { return a.W > a.top ? (size_t)a.N * a.H * a.W * 4 : 0; }
 
-cudaError_t launch_paged_select(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, cudaStream_t st) {
-  if (a.dtype == THIN_ATTN_FP32) return launch_e<float>(a, ids, keys, st);
-  if (a.dtype == THIN_ATTN_BF16) return launch_e<__nv_bfloat16>(a, ids, keys, st);
-  return launch_e<__half>(a, ids, keys, st);
+cudaError_t launch_paged_select(const thin_attn_paged_attention_args& a, int32_t* ids, int32_t* keys, void* workspace,
+                                cudaStream_t st) {
+  uint32_t* words = (uint32_t*)workspace;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (a.W > a.top) {   // else every page is taken
+    cudaError_t e = a.dtype == THIN_ATTN_FP32   ? score_e<float>(a, words, st)
+                    : a.dtype == THIN_ATTN_BF16 ? score_e<__nv_bfloat16>(a, words, st)
+                                                : score_e<__half>(a, words, st);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;
+  }
+  cfg.gridDim = dim3(a.H, a.N);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, select_kernel, a, (const uint32_t*)words, ids, keys);
 }
 
 }  // namespace thin
