@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "paged.h"
 #include "paged_types.cuh"
 
@@ -63,63 +65,105 @@ __device__ __forceinline__ void put_held(C* dst, const Held<C>& y) {
     for (int i = 0; i < Held<C>::kWords; i += 4) ((uint4*)dst)[i / 4] = make_uint4(y.w[i], y.w[i + 1], y.w[i + 2], y.w[i + 3]);
   }
 }
-// Their values, a NaN as 0.
-template <typename C>
-__device__ __forceinline__ void values_of(const Held<C>& y, float (&x)[8]) {
-  if constexpr (sizeof(C) == 1) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y.w[i / 4] >> (8 * (i & 3))), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = elem_f<C>(((const C*)y.w)[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] : 0.f;
-}
 
-// Minimum and maximum of a lane's 8 channels.
+// Minima and maxima run on the held values as they are: two 16-bit ones to a word (e4m3 as fp16, exactly),
+// or one fp32.
+template <typename C>
+struct Lane8 {
+  using M = typename std::conditional<sizeof(C) == 1, __half, C>::type;
+  static constexpr int kWords = sizeof(M) == 4 ? 8 : 4;
+  using V = typename std::conditional<sizeof(M) == 4, float, typename std::conditional<std::is_same<M, __half>::value, __half2, __nv_bfloat162>::type>::type;
+  V v[kWords];
+  static __device__ __forceinline__ V lesser(V a, V b) {
+    if constexpr (sizeof(M) == 4) return fminf(a, b); else return __hmin2(a, b);
+  }
+  static __device__ __forceinline__ V greater(V a, V b) {
+    if constexpr (sizeof(M) == 4) return fmaxf(a, b); else return __hmax2(a, b);
+  }
+  static __device__ __forceinline__ V everywhere(float x) {
+    if constexpr (sizeof(M) == 4) return x;
+    else if constexpr (std::is_same<M, __half>::value) return __half2half2(__float2half_rn(x));
+    else return __bfloat162bfloat162(__float2bfloat16_rn(x));
+  }
+  // A NaN as 0.
+  static __device__ __forceinline__ V number(V a) {
+    if constexpr (sizeof(M) == 4) {
+      return a == a ? a : 0.f;
+    } else {
+      const uint32_t w = *(const uint32_t*)&a & __heq2_mask(a, a);
+      return *(const V*)&w;
+    }
+  }
+  __device__ __forceinline__ void set(const Held<C>& y) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      V a;
+      if constexpr (sizeof(C) == 1) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y.w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        a = __half2(h);
+      } else {
+        a = *(const V*)&y.w[i];
+      }
+      v[i] = number(a);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(M) == 4) {
+        x[i] = v[i];
+      } else {
+        float2 f;
+        if constexpr (std::is_same<M, __half>::value) f = __half22float2(v[i]); else f = __bfloat1622float2(v[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+template <typename C>
 struct Range {
-  float lo[8], hi[8];
+  using L = Lane8<C>;
+  static constexpr int kWords = L::kWords;
+  L lo, hi;
   __device__ __forceinline__ Range() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = INFINITY;
-      hi[i] = -INFINITY;
+    for (int i = 0; i < kWords; ++i) {
+      lo.v[i] = L::everywhere(INFINITY);
+      hi.v[i] = L::everywhere(-INFINITY);
     }
   }
-  __device__ __forceinline__ void take(const float (&x)[8]) {
+  __device__ __forceinline__ void take(const L& l, const L& h) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = fminf(lo[i], x[i]);
-      hi[i] = fmaxf(hi[i], x[i]);
+    for (int i = 0; i < kWords; ++i) {
+      lo.v[i] = L::lesser(lo.v[i], l.v[i]);
+      hi.v[i] = L::greater(hi.v[i], h.v[i]);
     }
+  }
+  __device__ __forceinline__ void take(const Held<C>& y) {
+    L x;
+    x.set(y);
+    take(x, x);
   }
   // with lanes l and l + per, l + 2 per ...
   __device__ __forceinline__ void join(int per) {
     for (int o = per; o < 32; o <<= 1) {
+      L l, h;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      for (int i = 0; i < kWords; ++i) {
+        l.v[i] = __shfl_xor_sync(0xffffffffu, lo.v[i], o);
+        h.v[i] = __shfl_xor_sync(0xffffffffu, hi.v[i], o);
       }
+      take(l, h);
     }
   }
 };
 // Over tokens first, first + step, ... below last.
 template <typename T, typename C>
-__device__ __forceinline__ void range_of(const thin_attn_paged_append_args& a, Range& g, int first, int last, int step, int h, int col, float ks) {
+__device__ __forceinline__ void range_of(const thin_attn_paged_append_args& a, Range<C>& g, int first, int last, int step, int h, int col, float ks) {
   const T* src = (const T*)a.k + h * a.k_head + col;
 #pragma unroll 4
-  for (int t = first; t < last; t += step) {
-    float x[8];
-    values_of(held_of<T, C>(src + t * a.k_token, ks), x);
-    g.take(x);
-  }
+  for (int t = first; t < last; t += step) g.take(held_of<T, C>(src + t * a.k_token, ks));
 }
 
 struct Stored {
@@ -129,12 +173,15 @@ struct Stored {
 
 // A warp writes the bounds of one page and head: of `g` alone, or the stored ones widened.  Lanes of the same
 // channels hold the same range.
-__device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& a, const Range& g, const Stored& old, bool anew,
+template <typename C>
+__device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& a, const Range<C>& g, const Stored& old, bool anew,
                                              int64_t at, int col, bool writes, int lane) {
-  float m = 0.f;
+  float m = 0.f, lo[8], hi[8];
+  g.lo.floats(lo);
+  g.hi.floats(hi);
   if (col < a.E) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(g.lo[i]), fabsf(g.hi[i])));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -146,8 +193,8 @@ __device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& 
   uint32_t wl[2] = {0, 0}, wh[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int l = (int)fminf(fmaxf(floorf(g.lo[i] * inv), -127.f), 127.f);
-    int u = (int)fminf(fmaxf(ceilf(g.hi[i] * inv), -127.f), 127.f);
+    int l = (int)fminf(fmaxf(floorf(lo[i] * inv), -127.f), 127.f);
+    int u = (int)fminf(fmaxf(ceilf(hi[i] * inv), -127.f), 127.f);
     if (!anew) {
       const int sl = (int8_t)((i < 4 ? old.lo.x : old.lo.y) >> (8 * (i & 3))), sh = (int8_t)((i < 4 ? old.hi.x : old.hi.y) >> (8 * (i & 3)));
       l = min(l, sl >> up);
@@ -162,7 +209,7 @@ __device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& 
 }
 
 template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(thin_attn_paged_append_args a, int block, int k_shift, int v_shift) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) append_kernel(thin_attn_paged_append_args a, int block, int k_shift, int v_shift) {
   // k_shift, v_shift: 2^shift threads take a row, 8 elements each
   const int h = blockIdx.x % a.H, t0 = blockIdx.x / a.H * block, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ int page_s[kMany + 2], off_s[kMany];   // page_s[0]: the token before the block, [block + 1]: none
@@ -227,9 +274,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(thin_attn_paged_app
       }
     }
   }
-  // at most kMany / kShort runs of more than kShort tokens begin in a block; twice 256 floats for two of
-  // them where rows are wide, for four otherwise
-  __shared__ __align__(16) float part[kWarps * 2 * 512];
+  // of the runs that begin in a block all but the last end in it: at most four of 64 tokens have more than
+  // kShort, two of 32 (keys wider than 128: kPieces turns), one of kFew
+  constexpr int kLongs = 64;   // runs times threads of a row
+  __shared__ __align__(16) Lane8<C> part[kLongs * 2 * kWarps];
   const int per = 1 << k_shift, col = (lane & (per - 1)) * 8, sub = lane >> k_shift, rows = 32 >> k_shift;
   int shorts = 0, longs = 0;
   // bit i: token i begins a run, or goes to its page's first slot
@@ -268,31 +316,25 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(thin_attn_paged_app
       if (shorts++ % kWarps != warp) return;
       const int64_t at = (int64_t)pg * a.H + h;
       const Stored old = stored(at, anew);
-      Range g;
+      Range<C> g;
       if (col < a.E) range_of<T, C>(a, g, t0 + begin + sub, t0 + begin + n, rows, h, col, ks);
       g.join(per);
       write_bounds(a, g, old, anew, at, col, sub == 0, lane);
       return;
     }
-    Range g;
+    Range<C> g;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int r = k_row + u * k_step;
-      if (!has[u] || r < begin || r >= begin + n) continue;
-      float f[8];
-      values_of(x[u], f);
-      g.take(f);
+      if (has[u] && r >= begin && r < begin + n) g.take(x[u]);
     }
     if (begin + n > block && col < a.E)
       range_of<T, C>(a, g, t0 + block + warp * rows + sub, t0 + begin + n, kWarps * rows, h, col, ks);
     g.join(per);
     if (sub == 0 && col < a.E) {
-      float* dst = part + (longs * kWarps + warp) * 2 * a.E + col;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dst[k] = g.lo[k];
-        dst[a.E + k] = g.hi[k];
-      }
+      Lane8<C>* dst = part + (longs * kWarps + warp) * 2 * per + col / 8;
+      dst[0] = g.lo;
+      dst[per] = g.hi;
     }
     ++longs;
   });
@@ -303,16 +345,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(thin_attn_paged_app
     if (n <= kShort || longs++ % kWarps != warp) return;
     const int64_t at = (int64_t)pg * a.H + h;
     const Stored old = stored(at, anew);
-    Range g;
+    Range<C> g;
     if (col < a.E) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float* src = part + ((longs - 1) * kWarps + w) * 2 * a.E + col;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          g.lo[k] = fminf(g.lo[k], src[k]);
-          g.hi[k] = fmaxf(g.hi[k], src[a.E + k]);
-        }
+        const Lane8<C>* src = part + ((longs - 1) * kWarps + w) * 2 * per + col / 8;
+        g.take(src[0], src[per]);
       }
     }
     write_bounds(a, g, old, anew, at, col, sub == 0, lane);
