@@ -4,9 +4,33 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "thin_attn.h"
 
 namespace thin {
+
+// Lets `kernel` have up to `most` bytes of dynamic shared memory on the current device.  `most` is the same
+// at every call, so that calls from several threads cannot take the room from one another; the
+// runtime is asked once per device.
+class SharedMemory {
+ public:
+  cudaError_t allow(const void* kernel, int most) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < kDevices && granted_[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && dev < kDevices) granted_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<bool> granted_[kDevices] = {};
+};
+
+constexpr int kMaxRequests = 16384;   // of a plan, which keeps its sums in shared memory
+constexpr int kMaxGroup = 256;        // queries of a key head for page selection, for the same reason
 
 cudaError_t launch_paged_plan(const thin_attn_paged_plan_args& a, cudaStream_t st);
 cudaError_t launch_paged_release(const thin_attn_paged_release_args& a, cudaStream_t st);

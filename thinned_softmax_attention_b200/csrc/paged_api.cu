@@ -24,7 +24,6 @@ thin_attn_status err(thin_attn_status s, const char* fmt, ...) {
 }
 
 constexpr int64_t kIntMax = 0x7FFFFFFF;
-constexpr int kMaxRequests = 16384;   // the plan keeps its prefix sums in shared memory
 constexpr int kMaxTop = 4096;
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -72,7 +71,8 @@ thin_attn_status check_attention(const thin_attn_paged_attention_args* a) {
                  a->last, a->top);
     if (a->N > 65535 || a->H > 65535) return err(THIN_ATTN_EUNSUPPORTED, "page selection of %d tokens, %d heads: at most 65535", a->N, a->H);
     if ((int64_t)a->N * a->H * a->W > kIntMax) return err(THIN_ATTN_EUNSUPPORTED, "page selection over N * H * W = %lld pages", (long long)a->N * a->H * a->W);
-    if (a->Hq / a->H > 256) return err(THIN_ATTN_EUNSUPPORTED, "page selection with %d queries per key head: at most 256", a->Hq / a->H);
+    if (a->Hq / a->H > kMaxGroup)
+      return err(THIN_ATTN_EUNSUPPORTED, "page selection with %d queries per key head: at most %d", a->Hq / a->H, kMaxGroup);
   }
   return THIN_ATTN_OK;
 }

@@ -889,7 +889,8 @@ cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
   using S = Shape<Tile, C, HD, WARPS, STAGES>;
   static_assert((S::kSmem + 2048) * PER_SM <= 228 * 1024, "shared memory: with what the kernel declares and 1 KB of the driver's");
   auto kernel = attention_kernel<Tile, T, C, HD, WARPS, STAGES, PER_SM>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static SharedMemory memory;
+  cudaError_t e = memory.allow((const void*)kernel, S::kSmem);
   if (e != cudaSuccess) return e;
   const PartsLayout l = parts_layout(p.a);
   Parts parts{(float*)ws, (float*)((char*)ws + l.ml), (Cut*)((char*)ws + l.cuts)};

@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(thin_attn_paged_relea
 
 cudaError_t launch_paged_plan(const thin_attn_paged_plan_args& a, cudaStream_t st) {
   const size_t smem = (size_t)(2 * a.R + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SharedMemory memory;
+  cudaError_t e = memory.allow((const void*)plan_kernel, (2 * kMaxRequests + 1) * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
@@ -213,7 +214,8 @@ cudaError_t launch_paged_plan(const thin_attn_paged_plan_args& a, cudaStream_t s
 
 cudaError_t launch_paged_release(const thin_attn_paged_release_args& a, cudaStream_t st) {
   const size_t smem = (size_t)a.R * 4;
-  cudaError_t e = cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SharedMemory memory;
+  cudaError_t e = memory.allow((const void*)release_kernel, kMaxRequests * 4);
   if (e != cudaSuccess) return e;
   release_kernel<<<1, kThreads, smem, st>>>(a);
   return cudaGetLastError();

@@ -329,7 +329,8 @@ cudaError_t score_t(const thin_attn_paged_attention_args& a, uint32_t* words, cu
   if ((int64_t)((a.W + per - 1) / per) * a.N * a.H > 148 * 4) per = 512;
   const size_t smem = (size_t)rows * q_stride(a.E) + rows * 4;
   auto kernel = score_kernel<T, KJ>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SharedMemory memory;
+  cudaError_t e = memory.allow((const void*)kernel, kMaxGroup * (q_stride(256) + 4));
   if (e != cudaSuccess) return e;
   kernel<<<dim3((a.W + per - 1) / per, a.H, a.N), kWarps * 32, smem, st>>>(a, words, per);
   return cudaGetLastError();

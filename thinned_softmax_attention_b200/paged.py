@@ -30,6 +30,7 @@ _APPEND = struct.Struct("@I9iPqqPqqPPqqqPqqqPPPP")
 _ATTENTION = struct.Struct("@I16ifPqqPqqqPqqqPqPPPPPPPPqqPPN")
 
 _fns = None
+_stream = torch._C._cuda_getCurrentRawStream   # of a device ordinal; what current_stream(...).cuda_stream reads
 
 
 def _functions():
@@ -49,65 +50,73 @@ def _raise(status: int):
     _check(status)
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
+# The checks below cost a decode step as much as its kernels: they read each tensor's properties once, and
+# put messages together only when one of them fails.
 def _need(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _device(t: torch.Tensor, name: str) -> torch.device:
-    _need(t.is_cuda, f"{name}: expected a CUDA tensor, got one on {t.device}")
-    return t.device
+def _place(t: torch.Tensor) -> str:
+    return f"{t.dtype} {tuple(t.shape)} on {t.device}"
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: torch.device):
-    if t.dtype != dtype or t.device != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} ({n},) on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _index(t: torch.Tensor, name: str) -> int:
+    """Ordinal of the CUDA device that holds t."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return dev
 
 
-def _table(t: torch.Tensor, device: torch.device):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"table: expected int32 (R, W) with contiguous rows on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, dev: int) -> int:
+    """Address of a contiguous vector of n entries."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} ({n},) on cuda:{dev}, got {_place(t)}")
+    return t.data_ptr()
 
 
-def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: torch.device):
-    """(n_pages, H, page, E, D) of the pool."""
-    if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
-        raise ValueError(f"k_pages (n_pages, H, page, E) and v_pages (n_pages, H, page, D): got {tuple(k_pages.shape)} and {tuple(v_pages.shape)}")
-    if k_pages.dtype != v_pages.dtype or k_pages.device != device or v_pages.device != device:
-        raise ValueError(f"k_pages and v_pages: expected one type on {device}, got {k_pages.dtype} on {k_pages.device} and {v_pages.dtype} on {v_pages.device}")
-    if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
-        raise ValueError("k_pages and v_pages: the last axis must be contiguous")
-    return (*k_pages.shape, v_pages.shape[3])
+def _table(t: torch.Tensor, dev: int) -> Tuple[int, int, int]:
+    """(R, W, ids from row to row) of a block table."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not torch.int32 or t.get_device() != dev or len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
+        raise ValueError(f"table: expected int32 (R, W) with contiguous rows on cuda:{dev}, got {_place(t)}")
+    return shape[0], shape[1], strides[0]
+
+
+def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, dev: int):
+    """(n_pages, H, page, E, D) of the pool and its strides of pages, heads and rows."""
+    ks, vs, kt, vt = k_pages.shape, v_pages.shape, k_pages.stride(), v_pages.stride()
+    if (len(ks) != 4 or ks[:3] != vs[:3] or len(vs) != 4 or k_pages.dtype is not v_pages.dtype or k_pages.get_device() != dev
+            or v_pages.get_device() != dev or kt[3] != 1 or vt[3] != 1):
+        raise ValueError(f"k_pages (n_pages, H, page, E) and v_pages (n_pages, H, page, D): expected one type on cuda:{dev} and a "
+                         f"contiguous last axis, got {_place(k_pages)} and {_place(v_pages)}")
+    return ks, vs[3], kt, vt
 
 
 def _types(dtype: torch.dtype, cache: torch.dtype) -> Tuple[int, int]:
-    if dtype not in _DTYPES or dtype == torch.float8_e4m3fn:
+    dt, ct = _DTYPES.get(dtype, 3), _DTYPES.get(cache, -1)
+    if dt == 3:
         raise ValueError(f"dtype {dtype}: expected float32, bfloat16 or float16")
-    if cache != dtype and (cache != torch.float8_e4m3fn or dtype == torch.float32):
+    if ct != dt and (ct != 3 or dt == 0):
         raise ValueError(f"pages of {cache} with {dtype}: expected {dtype}, or float8_e4m3fn with bfloat16 or float16")
-    return _DTYPES[dtype], _DTYPES[cache]
+    return dt, ct
 
 
-def _scales(k_scale, v_scale, cache: torch.dtype, H: int, device: torch.device) -> Tuple[int, int]:
-    if cache != torch.float8_e4m3fn:
+def _scales(k_scale, v_scale, ct: int, H: int, dev: int) -> Tuple[int, int]:
+    if ct != 3:
         _need(k_scale is None and v_scale is None, "k_scale and v_scale belong to float8_e4m3fn pages")
         return 0, 0
     _need(k_scale is not None and v_scale is not None, "float8_e4m3fn pages need k_scale and v_scale")
-    _vector(k_scale, "k_scale", H, torch.float32, device)
-    _vector(v_scale, "v_scale", H, torch.float32, device)
-    return k_scale.data_ptr(), v_scale.data_ptr()
+    return _vector(k_scale, "k_scale", H, torch.float32, dev), _vector(v_scale, "v_scale", H, torch.float32, dev)
 
 
-def _bounds(bounds, n_pages: int, H: int, E: int, device: torch.device) -> Tuple[int, int]:
+def _bounds(bounds, n_pages: int, H: int, E: int, dev: int) -> Tuple[int, int]:
     lohi, exps = bounds
-    if lohi.dtype != torch.int8 or lohi.device != device or lohi.shape != (n_pages, H, 2, E) or not lohi.is_contiguous():
-        raise ValueError(f"bounds[0]: expected contiguous int8 {(n_pages, H, 2, E)} on {device}")
-    if exps.dtype != torch.int8 or exps.device != device or exps.shape != (n_pages, H) or not exps.is_contiguous():
-        raise ValueError(f"bounds[1]: expected contiguous int8 {(n_pages, H)} on {device}")
+    if lohi.dtype is not torch.int8 or lohi.get_device() != dev or lohi.shape != (n_pages, H, 2, E) or not lohi.is_contiguous():
+        raise ValueError(f"bounds[0]: expected contiguous int8 {(n_pages, H, 2, E)} on cuda:{dev}, got {_place(lohi)}")
+    if exps.dtype is not torch.int8 or exps.get_device() != dev or exps.shape != (n_pages, H) or not exps.is_contiguous():
+        raise ValueError(f"bounds[1]: expected contiguous int8 {(n_pages, H)} on cuda:{dev}, got {_place(exps)}")
     return lohi.data_ptr(), exps.data_ptr()
 
 
@@ -134,25 +143,23 @@ def paged_plan(lengths: torch.Tensor, new: torch.Tensor, table: torch.Tensor, fr
     in order; one that finds no room keeps its length and gets nothing (``status``).  The step's
     tokens are laid out request by request, ``max_tokens`` places in all.  ``lengths`` and
     ``n_free`` themselves change only with ``inplace=True``."""
-    dev = _device(lengths, "lengths")
-    R = lengths.shape[0]
-    _vector(lengths, "lengths", R, torch.int32, dev)
-    _vector(new, "new", R, torch.int32, dev)
-    _table(table, dev)
-    _need(table.shape[0] == R, f"table: {table.shape[0]} rows for {R} requests")
-    _vector(free, "free", free.numel(), torch.int32, dev)
-    _vector(n_free, "n_free", 1, torch.int32, dev)
-    _need(max_tokens >= 0 and page >= 1, f"page={page} and max_tokens={max_tokens}: expected page >= 1, max_tokens >= 0")
-    # one allocation: slots first (8 bytes each), then the 4-byte arrays
-    T = max_tokens
-    n32 = 2 * T + 2 * R + 1 + (0 if inplace else R + 1)
-    buf = torch.empty(2 * T + n32, dtype=torch.int32, device=dev)
-    slots = buf[:2 * T].view(torch.int64)
-    parts = buf[2 * T:].split([T, T, R + 1, R] + ([] if inplace else [R, 1]))
+    dev = _index(lengths, "lengths")
+    R, T = lengths.numel(), max_tokens
+    i32 = torch.int32
+    at = _vector(lengths, "lengths", R, i32, dev), _vector(new, "new", R, i32, dev)
+    rows_, W, row = _table(table, dev)
+    n_pages = free.numel()
+    pool = _vector(free, "free", n_pages, i32, dev), _vector(n_free, "n_free", 1, i32, dev)
+    if rows_ != R or T < 0 or page < 1:
+        raise ValueError(f"table of {rows_} rows, {R} requests, page={page}, max_tokens={T}: expected a row per request, page >= 1, "
+                         "max_tokens >= 0")
+    device = lengths.device
+    slots = torch.empty(T, dtype=torch.int64, device=device)
+    sizes = (T, T, R + 1, R) if inplace else (T, T, R + 1, R, R, 1)
+    parts = torch.split_with_sizes(torch.empty(sum(sizes), dtype=i32, device=device), sizes)   # one allocation
     rows, context, cu, status = parts[:4]
     lengths_out, n_free_out = (lengths, n_free) if inplace else parts[4:]
-    p = _PLAN.pack(_PLAN.size, dev.index, R, table.shape[1], page, free.numel(), T, 0, lengths.data_ptr(), new.data_ptr(),
-                   table.data_ptr(), table.stride(0), free.data_ptr(), n_free.data_ptr(), lengths_out.data_ptr(),
+    p = _PLAN.pack(_PLAN.size, dev, R, W, page, n_pages, T, 0, *at, table.data_ptr(), row, *pool, lengths_out.data_ptr(),
                    n_free_out.data_ptr(), cu.data_ptr(), slots.data_ptr(), rows.data_ptr(), context.data_ptr(),
                    status.data_ptr())
     s = _functions().thin_attn_paged_plan(p, _stream(dev))
@@ -165,16 +172,13 @@ def paged_release(keep: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor
                   n_free: torch.Tensor, page: int) -> None:
     """Shorten request r to ``keep[r]`` tokens (0: it has ended; negative: as it is) and give the pages
     behind them back; lengths, table, free and n_free change in place."""
-    dev = _device(lengths, "lengths")
-    R = lengths.shape[0]
-    _vector(lengths, "lengths", R, torch.int32, dev)
-    _vector(keep, "keep", R, torch.int32, dev)
-    _table(table, dev)
-    _need(table.shape[0] == R, f"table: {table.shape[0]} rows for {R} requests")
-    _vector(free, "free", free.numel(), torch.int32, dev)
-    _vector(n_free, "n_free", 1, torch.int32, dev)
-    p = _RELEASE.pack(_RELEASE.size, dev.index, R, table.shape[1], page, free.numel(), keep.data_ptr(), lengths.data_ptr(),
-                      table.data_ptr(), table.stride(0), free.data_ptr(), n_free.data_ptr())
+    dev = _index(lengths, "lengths")
+    R, i32 = lengths.numel(), torch.int32
+    at = _vector(keep, "keep", R, i32, dev), _vector(lengths, "lengths", R, i32, dev)
+    rows, W, row = _table(table, dev)
+    _need(rows == R and page >= 1, f"table of {rows} rows, {R} requests, page={page}: expected a row per request, page >= 1")
+    pool = _vector(free, "free", free.numel(), i32, dev), _vector(n_free, "n_free", 1, i32, dev)
+    p = _RELEASE.pack(_RELEASE.size, dev, R, W, page, free.numel(), *at, table.data_ptr(), row, *pool)
     s = _functions().thin_attn_paged_release(p, _stream(dev))
     if s:
         _raise(s)
@@ -189,21 +193,19 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     ``bounds`` = (int8 (n_pages, H, 2, E), int8 (n_pages, H)): the pages' key bounds for
     ``paged_sparse_attention``, widened by the new keys, or started anew where a page's first slot
     is written; the tokens of one page must then be neighbours, as ``paged_plan`` lays them."""
-    dev = _device(k, "k")
-    P, H, page, E, D = _pool(k_pages, v_pages, dev)
-    N = k.shape[0]
-    if k.shape != (N, H, E) or v.shape != (N, H, D) or k.dtype != v.dtype or v.device != dev:
-        raise ValueError(f"k and v: expected {(N, H, E)} and {(N, H, D)} of one type on {dev}, got {k.dtype} {tuple(k.shape)} "
-                         f"and {v.dtype} {tuple(v.shape)} on {v.device}")
-    if k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("k and v: the last axis must be contiguous")
-    _vector(slots, "slots", N, torch.int64, dev)
+    dev = _index(k, "k")
+    (P, H, page, E), D, kt, vt = _pool(k_pages, v_pages, dev)
+    N, kst, vst = k.shape[0], k.stride(), v.stride()
+    if (k.shape != (N, H, E) or v.shape != (N, H, D) or k.dtype is not v.dtype or v.get_device() != dev or kst[2] != 1
+            or vst[2] != 1):
+        raise ValueError(f"k and v: expected {(N, H, E)} and {(N, H, D)} of one type on cuda:{dev} with a contiguous last axis, got "
+                         f"{_place(k)} and {_place(v)}")
+    at = _vector(slots, "slots", N, torch.int64, dev)
     dt, ct = _types(k.dtype, k_pages.dtype)
-    ks, vs = _scales(k_scale, v_scale, k_pages.dtype, H, dev)
+    ks, vs = _scales(k_scale, v_scale, ct, H, dev)
     b, x = (0, 0) if bounds is None else _bounds(bounds, P, H, E, dev)
-    p = _APPEND.pack(_APPEND.size, dev.index, dt, ct, N, H, E, D, page, P, k.data_ptr(), *k.stride()[:2], v.data_ptr(),
-                     *v.stride()[:2], slots.data_ptr(), k_pages.data_ptr(), *k_pages.stride()[:3], v_pages.data_ptr(),
-                     *v_pages.stride()[:3], ks, vs, b, x)
+    p = _APPEND.pack(_APPEND.size, dev, dt, ct, N, H, E, D, page, P, k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1], at,
+                     k_pages.data_ptr(), kt[0], kt[1], kt[2], v_pages.data_ptr(), vt[0], vt[1], vt[2], ks, vs, b, x)
     s = _functions().thin_attn_paged_append(p, _stream(dev))
     if s:
         _raise(s)
@@ -219,42 +221,50 @@ def _workspace_bytes(dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, 
 
 
 def _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, window, bounds, top, first, last, out,
-               lse, pages):
-    dev = _device(q, "q")
-    P, H, page, E, D = _pool(k_pages, v_pages, dev)
-    if q.dim() != 3 or q.shape[2] != E or q.stride(2) != 1:
-        raise ValueError(f"q: expected (N, Hq, {E}) with a contiguous last axis, got {tuple(q.shape)}")
-    N, Hq, _ = q.shape
-    _need(Hq % H == 0 and Hq >= H, f"{Hq} query heads over {H} key heads")
-    _table(table, dev)
-    R, W = table.shape
-    _vector(lengths, "lengths", N, torch.int32, dev)
-    if rows is not None:
-        _vector(rows, "rows", N, torch.int32, dev)
+               lse, return_lse, return_pages):
+    """(out, lse, pages): the last two None unless asked for."""
+    dev = _index(q, "q")
+    (P, H, page, E), D, kt, vt = _pool(k_pages, v_pages, dev)
+    shape, qst = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != E or qst[2] != 1 or shape[1] % H or not shape[1]:
+        raise ValueError(f"q: expected (N, Hq, {E}) with a contiguous last axis, Hq a multiple of {H}, got {_place(q)}")
+    N, Hq, _ = shape
+    R, W, row = _table(table, dev)
+    seen = _vector(lengths, "lengths", N, torch.int32, dev)
+    of = 0 if rows is None else _vector(rows, "rows", N, torch.int32, dev)
     dt, ct = _types(q.dtype, k_pages.dtype)
-    ks, vs = _scales(k_scale, v_scale, k_pages.dtype, H, dev)
+    ks, vs = _scales(k_scale, v_scale, ct, H, dev)
+    device = q.device
+    # rows of padding tokens are not written: zeros there where the buffer is made here
+    make = torch.empty if rows is None else torch.zeros
     if out is None:
-        # rows of padding tokens are not written: zeros there when the buffer is made here
-        out = (torch.empty if rows is None else torch.zeros)((N, Hq, D), dtype=q.dtype, device=dev)
-    elif out.shape != (N, Hq, D) or out.dtype != q.dtype or out.device != dev or out.stride(2) != 1:
-        raise ValueError(f"out: expected {q.dtype} {(N, Hq, D)} with a contiguous last axis on {dev}")
-    if lse is not None and (lse.shape != (N, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev):
-        raise ValueError(f"lse: expected contiguous float32 {(N, Hq)} on {dev}, got {lse.dtype} {tuple(lse.shape)}")
+        out = torch.empty_like(q) if rows is None and D == E and q.is_contiguous() else make((N, Hq, D), dtype=q.dtype, device=device)
+    ost = out.stride()
+    if out.shape != (N, Hq, D) or out.dtype is not q.dtype or out.get_device() != dev or ost[2] != 1:
+        raise ValueError(f"out: expected {q.dtype} {(N, Hq, D)} with a contiguous last axis on cuda:{dev}, got {_place(out)}")
+    if lse is None:
+        if return_lse:
+            lse = make((N, Hq), dtype=torch.float32, device=device)
+    elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError(f"lse: expected contiguous float32 {(N, Hq)} on cuda:{dev}, got {_place(lse)}")
     b, x = (0, 0) if bounds is None else _bounds(bounds, P, H, E, dev)
+    pages = None
+    if return_pages:
+        pages = torch.empty((N, H, top), dtype=torch.int32, device=device) if rows is None else torch.full(
+            (N, H, top), -1, dtype=torch.int32, device=device)
     n = _workspace_bytes(dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last, rows is not None)
     # scratch of this call alone: the caching allocator hands it on in stream order, and a capture
     # gets its own from the graph's pool
-    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    p = _ATTENTION.pack(_ATTENTION.size, dev.index, dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last,
-                        0.0 if scale is None else scale, q.data_ptr(), q.stride(0), q.stride(1), k_pages.data_ptr(),
-                        *k_pages.stride()[:3], v_pages.data_ptr(), *v_pages.stride()[:3], table.data_ptr(), table.stride(0),
-                        lengths.data_ptr(), 0 if rows is None else rows.data_ptr(), ks, vs, b, x,
-                        0 if pages is None else pages.data_ptr(), out.data_ptr(), out.stride(0), out.stride(1),
-                        0 if lse is None else lse.data_ptr(), 0 if ws is None else ws.data_ptr(), n)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    p = _ATTENTION.pack(_ATTENTION.size, dev, dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last,
+                        0.0 if scale is None else scale, q.data_ptr(), qst[0], qst[1], k_pages.data_ptr(), kt[0], kt[1], kt[2],
+                        v_pages.data_ptr(), vt[0], vt[1], vt[2], table.data_ptr(), row, seen, of, ks, vs, b, x,
+                        0 if pages is None else pages.data_ptr(), out.data_ptr(), ost[0], ost[1],
+                        0 if lse is None else lse.data_ptr(), ws.data_ptr(), n)
     s = _functions().thin_attn_paged_attention(p, _stream(dev))
     if s:
         _raise(s)
-    return out
+    return out, lse, pages
 
 
 def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
@@ -271,15 +281,9 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     nothing gets zeros and -inf; one whose row is negative is padding and leaves its rows of
     ``out`` and ``lse`` as they were (zeros in buffers made here).
     The keys are read once per query token: made for decode and short drafts, not for long prompts."""
-    if lse is None and return_lse:
-        lse = _new_lse(q, rows)
-    out = _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, window, None, 0, 0, 0, out, lse, None)
+    out, lse, _ = _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, window, None, 0, 0, 0, out, lse,
+                             return_lse, False)
     return out if lse is None else (out, lse)
-
-
-def _new_lse(q: torch.Tensor, rows) -> torch.Tensor:
-    _device(q, "q")
-    return (torch.empty if rows is None else torch.zeros)(q.shape[:2], dtype=torch.float32, device=q.device)
 
 
 def paged_sparse_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
@@ -292,16 +296,9 @@ def paged_sparse_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     ``first`` and last ``last`` ones, and those whose ``bounds`` (``paged_append``) promise the largest
     q . k to any of the head's queries.  Returns out, then lse and pages as asked; pages (N, H, top)
     int32 holds the chosen pages' places in the request in ascending order, then -1."""
-    if lse is None and return_lse:
-        lse = _new_lse(q, rows)
     _need(top >= 1, f"top={top}: expected at least one page")
-    pages = None
-    if return_pages:
-        pages = torch.empty((q.shape[0], k_pages.shape[1], top), dtype=torch.int32, device=q.device)
-        if rows is not None:
-            pages.fill_(-1)
-    out = _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, 0, bounds, top, first, last, out,
-                     lse, pages)
+    out, lse, pages = _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, 0, bounds, top, first, last,
+                                 out, lse, return_lse, return_pages)
     got = (out,) + ((lse,) if lse is not None else ()) + ((pages,) if return_pages else ())
     return got if len(got) > 1 else out
 
@@ -324,8 +321,7 @@ class PagedAttentionCache:
         ct = cache_dtype or dtype
         _need(min(n_pages, page, H, E, D, max_requests, max_length) >= 1,
               f"n_pages={n_pages} page={page} H={H} E={E} D={D} max_requests={max_requests} max_length={max_length}: all >= 1")
-        _types(dtype, ct)
-        _scales(k_scale, v_scale, ct, H, dev)
+        _scales(k_scale, v_scale, _types(dtype, ct)[1], H, device)
         self.dtype, self.device, self.page, self.scale = dtype, dev, page, scale
         self.k_scale, self.v_scale = k_scale, v_scale
         self.k_pages = torch.zeros((n_pages, H, page, E), dtype=ct, device=dev)
