@@ -2,52 +2,57 @@
 //
 // A plan is two prefix sums over the requests (their new tokens; the fresh pages of those whose
 // tokens and table rows have room), then one slot per token:
-//   request  the r with cu[r] <= t < cu[r + 1], by binary search of the sums in shared memory
-//   page     table[r][pos / page], or for a fresh page free[n_free - 1 - (fresh pages before it)]
+//   request  the r with cu[r] <= t < cu[r + 1], by binary search of the sums
+//   page     table[r][pos / page], once the fresh pages, free[n_free - 1 - (those before it)], are in the table
 //   slot     page id * page + pos % page
 // Nothing here moves more than a few bytes per request and 16 per token: the time is the chain of
-// dependent latencies (lengths, sums, search, page id).  Every CTA of a cluster repeats the sums
-// for itself, so the only meeting is the one before lengths and n_free are overwritten in place.
-#include <cooperative_groups.h>
-
+// dependent latencies (lengths, sums, search, page id), so one CTA takes it all while the tokens are few,
+// and a second launch spreads the tokens over the GPU when they are many.  Both sums are taken at
+// once, as if every token had room; only where one has not are the pages summed again.
 #include "paged.h"
-
-namespace cg = cooperative_groups;
 
 namespace thin {
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kCluster = 8;   // the largest portable cluster
+constexpr int kThreads = 1024, kFewThreads = 256;   // of the first launch
+constexpr int kFillHere = 2048;                     // tokens that it places itself
+constexpr int kFillThreads = 256;
+constexpr int kOwnPages = 2;                        // fresh pages that a request's thread enters itself
 
-// Exclusive prefix of v over the block's threads and the total.
-__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* warp_sums, int64_t* total) {
+struct Sums {
+  int64_t tokens, pages;
+};
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.tokens + b.tokens, a.pages + b.pages}; }
+__device__ __forceinline__ Sums operator-(Sums a, Sums b) { return {a.tokens - b.tokens, a.pages - b.pages}; }
+
+// Exclusive prefix of v over the block's threads, and the total.
+__device__ __forceinline__ Sums block_prefix(Sums v, Sums* warp_sums, Sums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
+  Sums incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const Sums y = {__shfl_up_sync(0xffffffffu, incl.tokens, o), __shfl_up_sync(0xffffffffu, incl.pages, o)};
+    if (lane >= o) incl = incl + y;
   }
   __syncthreads();   // the sums of an earlier call have been read
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    int64_t s = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
+  // every warp adds the warps' sums up for itself
+  Sums w = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : Sums{0, 0};
+  Sums before = lane < warp ? w : Sums{0, 0};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
+  for (int o = 16; o; o >>= 1) {
+    w = w + Sums{__shfl_xor_sync(0xffffffffu, w.tokens, o), __shfl_xor_sync(0xffffffffu, w.pages, o)};
+    before = before + Sums{__shfl_xor_sync(0xffffffffu, before.tokens, o), __shfl_xor_sync(0xffffffffu, before.pages, o)};
   }
-  __syncthreads();
-  *total = warp_sums[(blockDim.x >> 5) - 1];
-  return incl - v + (warp ? warp_sums[warp - 1] : 0);
+  *total = w;
+  return incl - v + before;
 }
 
-__device__ __forceinline__ int64_t pages_of(int64_t tokens, int page) { return (tokens + page - 1) / page; }
+__device__ __forceinline__ int64_t pages_of(int64_t tokens, int page) {
+  return tokens < 0x7FFF0000 ? ((uint32_t)tokens + page - 1) / (uint32_t)page : (tokens + page - 1) / page;
+}
 
 struct Request {
   int64_t have, want;   // pages before and after
@@ -65,97 +70,119 @@ __device__ __forceinline__ Request request(const thin_attn_paged_plan_args& a, i
   return q;
 }
 
+// Writes slot, request and context of place t.  cu(r): the sums; length(r): the request's length before the
+// step, negative when it was not placed.
+template <typename Cu, typename Length>
+__device__ __forceinline__ void put_token(const thin_attn_paged_plan_args& a, int t, Cu&& cu, Length&& length) {
+  int64_t slot = -1;
+  int row = -1, context = 0;
+  if (t < cu(a.R)) {
+    int lo = 0, hi = a.R;   // the last r with cu[r] <= t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu(mid) <= t) lo = mid; else hi = mid;
+    }
+    const int L = length(lo);
+    if (L >= 0) {
+      const int pos = L + t - cu(lo), j = (int)((uint32_t)pos / (uint32_t)a.page);
+      slot = (int64_t)a.table[lo * a.table_row + j] * a.page + (pos - j * a.page);
+      row = lo;
+      context = pos + 1;
+    }
+  }
+  a.slots[t] = slot;
+  a.rows[t] = row;
+  a.context[t] = context;
+}
+
 __global__ void __launch_bounds__(kThreads) plan_kernel(thin_attn_paged_plan_args a) {
   extern __shared__ int32_t smem[];
-  __shared__ int64_t warp_sums[32];
-  int32_t* cu_s = smem;              // R + 1
-  int32_t* base_s = smem + a.R + 1;  // fresh pages before the request's own, -1 when it is not placed
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int per = (a.R + kThreads - 1) / kThreads;
-  const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
+  __shared__ Sums warp_sums[32];
+  __shared__ int taken_s;
+  int32_t* cu_s = smem;                 // R + 1
+  int32_t* length_s = cu_s + a.R + 1;   // R: before the step, -1 when the request is not placed
+  int32_t* base_s = length_s + a.R;     // R: fresh pages before its own
+  const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 31;
+  // the filling launch may be set up now; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per = (a.R + threads - 1) / threads;
+  const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
   const int64_t n_free = min(max(*a.n_free, 0), a.n_pages);
-  int64_t tokens = 0;
-  for (int r = r0; r < r1; ++r) tokens += request(a, r).n;
-  int64_t all_tokens, all_pages;
-  const int64_t first = block_prefix(tokens, warp_sums, &all_tokens);
-  int64_t pages = 0, at = first;
+  if (tid == 0) taken_s = 0;
+  Sums mine = {0, 0}, all;
   for (int r = r0; r < r1; ++r) {
     const Request q = request(a, r);
-    at += q.n;
-    if (!q.narrow && at <= a.max_tokens) pages += q.want - q.have;
+    mine = mine + Sums{q.n, q.narrow ? 0 : q.want - q.have};
   }
-  int64_t base = block_prefix(pages, warp_sums, &all_pages);
-  at = first;
-  int64_t taken = 0;   // pages that this thread's placed requests take
-  for (int r = r0; r < r1; ++r) {
-    const Request q = request(a, r);
-    cu_s[r] = (int32_t)min(at, (int64_t)0x7FFFFFFF);
-    at += q.n;
-    const bool late = !q.narrow && at > a.max_tokens;
-    const int64_t need = q.narrow || late ? 0 : q.want - q.have;
-    const bool dry = need > 0 && base + need > n_free;
-    const int status = q.narrow ? 2 : late ? 3 : dry ? 1 : 0;
-    base_s[r] = status ? -1 : (int32_t)base;
-    if (!status) taken += need;
-    base += need;
-    if (rank == 0) {
-      a.status[r] = status;
-      a.cu[r] = cu_s[r];
+  Sums at = block_prefix(mine, warp_sums, &all);
+  if (all.tokens > a.max_tokens) {   // for every thread alike
+    int64_t t = at.tokens;
+    mine.pages = 0;
+    for (int r = r0; r < r1; ++r) {
+      const Request q = request(a, r);
+      t += q.n;
+      if (!q.narrow && t <= a.max_tokens) mine.pages += q.want - q.have;
     }
+    at = block_prefix(mine, warp_sums, &all);
   }
-  int64_t all_taken;
-  block_prefix(taken, warp_sums, &all_taken);
-  if (threadIdx.x == 0) {
-    cu_s[a.R] = (int32_t)min(all_tokens, (int64_t)0x7FFFFFFF);
-    if (rank == 0) a.cu[a.R] = cu_s[a.R];
-  }
-  __syncthreads();
-  // fresh table entries, a warp per request
-  const int warps = ranks * (kThreads / 32), warp = rank * (kThreads / 32) + (int)(threadIdx.x >> 5);
-  for (int r = warp; r < a.R; r += warps) {
-    if (base_s[r] < 0) continue;
+  int taken = 0;   // pages taken up to this thread's last placed request
+  bool many = false;
+  for (int r = r0; r < r1; ++r) {
     const Request q = request(a, r);
-    for (int64_t j = q.have + (threadIdx.x & 31); j < q.want; j += 32)
-      a.table[r * a.table_row + j] = a.free_pages[n_free - 1 - (base_s[r] + j - q.have)];
+    const int cu = (int)min(at.tokens, (int64_t)0x7FFFFFFF);
+    at.tokens += q.n;
+    const bool late = !q.narrow && at.tokens > a.max_tokens;
+    const int64_t need = q.narrow || late ? 0 : q.want - q.have, base = at.pages;
+    at.pages += need;
+    const int status = q.narrow ? 2 : late ? 3 : need > 0 && at.pages > n_free ? 1 : 0;
+    if (status == 0 && need > 0) {
+      taken = (int)at.pages;
+      many |= need > kOwnPages;
+      if (need <= kOwnPages)
+        for (int64_t j = 0; j < need; ++j) a.table[r * a.table_row + q.have + j] = a.free_pages[n_free - 1 - (base + j)];
+    }
+    cu_s[r] = cu;
+    length_s[r] = status ? -1 : q.L;
+    base_s[r] = (int)min(base, (int64_t)0x7FFFFFFF);
+    a.status[r] = status;
+    a.cu[r] = cu;
+    a.lengths_out[r] = status ? q.L : q.L + q.n;   // lengths[r] is read by this thread alone
   }
-  // the tokens' slots
-  const int live = min(cu_s[a.R], a.max_tokens);
-  for (int t = rank * kThreads + (int)threadIdx.x; t < a.max_tokens; t += ranks * kThreads) {
-    int64_t slot = -1;
-    int row = -1, context = 0;
-    if (t < live) {
-      int lo = 0, hi = a.R;   // the last r with cu[r] <= t
+  taken = __reduce_max_sync(0xffffffffu, taken);
+  if (lane == 0 && taken) atomicMax(&taken_s, taken);
+  if (tid == 0) cu_s[a.R] = a.cu[a.R] = (int)min(all.tokens, (int64_t)0x7FFFFFFF);
+  if (__syncthreads_or(many)) {
+    // the e-th page taken goes to the last request with base <= e (one that takes none shares its base with
+    // the next; behind the last placed request no base is below the pages taken)
+    for (int e = tid; e < taken_s; e += threads) {
+      int lo = 0, hi = a.R;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cu_s[mid] <= t) lo = mid; else hi = mid;
+        if (base_s[mid] <= e) lo = mid; else hi = mid;
       }
-      if (base_s[lo] >= 0) {
-        const int L = a.lengths[lo], pos = L + t - cu_s[lo], j = pos / a.page, have = (int)pages_of(L, a.page);
-        const int id = j < have ? a.table[lo * a.table_row + j] : a.free_pages[n_free - 1 - (base_s[lo] + j - have)];
-        slot = (int64_t)id * a.page + pos % a.page;
-        row = lo;
-        context = pos + 1;
-      }
+      a.table[lo * a.table_row + pages_of(length_s[lo], a.page) + e - base_s[lo]] = a.free_pages[n_free - 1 - e];
     }
-    a.slots[t] = slot;
-    a.rows[t] = row;
-    a.context[t] = context;
+    __syncthreads();
   }
-  cluster.sync();   // every CTA has read lengths and n_free
-  if (rank != 0) return;
-  for (int r = threadIdx.x; r < a.R; r += kThreads) {
-    const int32_t L = a.lengths[r];
-    a.lengths_out[r] = base_s[r] < 0 ? L : L + max(a.n_new[r], 0);
-  }
-  if (threadIdx.x == 0) *a.n_free_out = (int32_t)(n_free - all_taken);
+  if (tid == 0) *a.n_free_out = (int32_t)(n_free - taken_s);
+  if (a.max_tokens <= kFillHere)
+    for (int t = tid; t < a.max_tokens; t += threads)
+      put_token(a, t, [&](int r) { return cu_s[r]; }, [&](int r) { return length_s[r]; });
+}
+
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(thin_attn_paged_plan_args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = blockIdx.x * kFillThreads + threadIdx.x;
+  if (t >= a.max_tokens) return;
+  put_token(a, t, [&](int r) { return a.cu[r]; },
+            [&](int r) { return a.status[r] ? -1 : a.lengths_out[r] - (a.cu[r + 1] - a.cu[r]); });
 }
 
 // One CTA: the released pages' prefix sums give each its place on the stack.
 __global__ void __launch_bounds__(kThreads) release_kernel(thin_attn_paged_release_args a) {
-  __shared__ int64_t warp_sums[32];
+  __shared__ Sums warp_sums[32];
   extern __shared__ int32_t base_s[];   // R
-  const int per = (a.R + kThreads - 1) / kThreads;
+  const int threads = blockDim.x, per = (a.R + threads - 1) / threads;
   const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
   const int64_t n_free = min(max(*a.n_free, 0), a.n_pages);
   auto kept = [&](int r, int64_t* from, int64_t* to) {
@@ -164,19 +191,20 @@ __global__ void __launch_bounds__(kThreads) release_kernel(thin_attn_paged_relea
     *from = min(pages_of(keep, a.page), *to);
     return (int32_t)keep;
   };
-  int64_t pages = 0, from, to, total;
+  Sums mine = {0, 0}, all;
+  int64_t from, to;
   for (int r = r0; r < r1; ++r) {
     kept(r, &from, &to);
-    pages += to - from;
+    mine.pages += to - from;
   }
-  int64_t base = block_prefix(pages, warp_sums, &total);
+  int64_t base = block_prefix(mine, warp_sums, &all).pages;
   for (int r = r0; r < r1; ++r) {
     kept(r, &from, &to);
     base_s[r] = (int32_t)min(base, (int64_t)a.n_pages);
     base += to - from;
   }
   __syncthreads();
-  for (int r = threadIdx.x >> 5; r < a.R; r += kThreads / 32) {
+  for (int r = threadIdx.x >> 5; r < a.R; r += threads >> 5) {
     const int32_t keep = kept(r, &from, &to);
     for (int64_t j = from + (threadIdx.x & 31); j < to; j += 32) {
       const int64_t at = n_free + base_s[r] + j - from;
@@ -188,36 +216,36 @@ __global__ void __launch_bounds__(kThreads) release_kernel(thin_attn_paged_relea
     if ((threadIdx.x & 31) == 0 && a.lengths[r] >= 0) a.lengths[r] = keep;
   }
   __syncthreads();
-  if (threadIdx.x == 0) *a.n_free = (int32_t)min(n_free + total, (int64_t)a.n_pages);
+  if (threadIdx.x == 0) *a.n_free = (int32_t)min(n_free + all.pages, (int64_t)a.n_pages);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_plan(const thin_attn_paged_plan_args& a, cudaStream_t st) {
-  const size_t smem = (size_t)(2 * a.R + 1) * 4;
   static SharedMemory memory;
-  cudaError_t e = memory.allow((const void*)plan_kernel, (2 * kMaxRequests + 1) * 4);
+  cudaError_t e = memory.allow((const void*)plan_kernel, (3 * kMaxRequests + 1) * 4);
   if (e != cudaSuccess) return e;
+  const int threads = a.R <= kFewThreads && a.max_tokens <= 2 * kFewThreads ? kFewThreads : kThreads;
+  plan_kernel<<<1, threads, (size_t)(3 * a.R + 1) * 4, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.max_tokens <= kFillHere) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(kCluster);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((a.max_tokens + kFillThreads - 1) / kFillThreads);
+  cfg.blockDim = dim3(kFillThreads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, fill_kernel, a);
 }
 
 cudaError_t launch_paged_release(const thin_attn_paged_release_args& a, cudaStream_t st) {
-  const size_t smem = (size_t)a.R * 4;
   static SharedMemory memory;
   cudaError_t e = memory.allow((const void*)release_kernel, kMaxRequests * 4);
   if (e != cudaSuccess) return e;
-  release_kernel<<<1, kThreads, smem, st>>>(a);
+  release_kernel<<<1, a.R <= kFewThreads ? kFewThreads : kThreads, (size_t)a.R * 4, st>>>(a);
   return cudaGetLastError();
 }
 
