@@ -100,8 +100,8 @@ def attention(q, K, V, scale=None):
     return p @ V, lse, p @ V.abs(), dz
 
 
-# How exactly the kernels keep the weights p before the product with V.
-P_STEP = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -16, "fp16": 2.0 ** -16, "e4m3": 2.0 ** -11}
+# How exactly the kernels keep p and V in their product (fp32: each as two tf32 numbers, 2^-22 both).
+P_STEP = {"fp32": 2.0 ** -21, "bf16": 2.0 ** -16, "fp16": 2.0 ** -16, "e4m3": 2.0 ** -11}
 
 
 def tolerance(ref, lse, spread, dz, n_keys, dtype, cache):

@@ -207,11 +207,14 @@ def test_extreme_scores(dtype):
             kp[int(table[r, j // page]), 0, j % page, 0] = x
     out = T.paged_attention(q, kp, vp, table, i32([L] * 3))
     v = held[0][1][0].to(TYPES[dtype])
-    assert torch.equal(out[0], v[37].expand(G, D))
+    # a weight of 1: the value itself; an fp32 value enters the product as hi + lo with lo cut to 11 of its 12
+    # bits, so it may lose 2^-23 of its leading bit, and hi + lo' is exact in fp32
+    near = lambda a, b: ((a.double() - b.double()).abs() <= (2.0 ** -23 * b.double().abs() if dtype == "fp32" else 0)).all()
+    assert near(out[0], v[37].expand(G, D))
     mean = held[1][1][0].mean(0)
     tol = torch.finfo(TYPES[dtype]).eps * mean.abs() + (2.0 ** -16 + 2 * L * 2.0 ** -24) * held[1][1][0].abs().mean(0)
     assert ((out[1].double() - mean).abs() <= tol).all()
-    assert torch.equal(out[2], held[2][1][0].to(TYPES[dtype])[3].expand(G, D))
+    assert near(out[2], held[2][1][0].to(TYPES[dtype])[3].expand(G, D))
 
 
 def bounds_of(kp, table, lengths, page):

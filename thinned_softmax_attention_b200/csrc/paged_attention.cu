@@ -24,7 +24,9 @@
 // (of d = DC (r + 8 i) ..) and pairs them up with byte permutations.  No transposing load, no shuffle but
 // the row maximum.  G <= 8 leaves the tile's upper 8 rows free: they carry P's rounding error, so P
 // keeps 16 bits and more at no cost; G <= 16 issues that product separately (16-bit caches).
-// fp32 caches run on CUDA cores in fp32.
+//
+// fp32 caches use the tf32 products (m16n8k8) with every operand as the sum of two tf32 numbers,
+// (a_hi + a_lo)(b_hi + b_lo), good to 2^-22.  The upper rows of the tile carry a_lo, so that takes two products.
 #include <type_traits>
 
 #include "paged.h"
@@ -34,7 +36,7 @@ namespace thin {
 
 namespace {
 
-constexpr int kKeys = 16;          // keys of a warp's stage
+constexpr int kAlign = 16;         // keys before a window that its first stage may hold
 constexpr int kMaxCtas = 444;      // 148 SMs x 3
 
 // One token of the call: its row of outputs, its visible keys [start, len) and their units.
@@ -55,7 +57,7 @@ __device__ __forceinline__ Token token_from(const PagedAttn& p, int n, int row, 
   t.live = row >= 0 && row < p.a.R;
   t.len = t.live ? min(max(len, 0), p.list_width * p.a.page) : 0;
   t.start = p.a.window && t.len > p.a.window ? t.len - p.a.window : 0;
-  const int first = t.start & ~(kKeys - 1);
+  const int first = t.start & ~(kAlign - 1);
   t.units = (t.len - first + UNIT - 1) / UNIT;
   t.ids = p.ids + (p.list_rows ? row : n) * p.ids_token;
   return t;
@@ -87,11 +89,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// Rows of a stage lie one behind the other; the 16-byte pieces of a row are permuted within groups of
-// eight so that the fragment reads below meet every bank once: K's quarter-warps read the same pieces of two
-// neighbouring rows, V's two neighbouring pieces of rows 4 apart.
-__device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) ^ (((row >> 2) & 3) << 1); }
 
 template <typename M>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -130,7 +127,7 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 // ---------------------------------------------------------------------------------------------
 template <typename T, typename C, int HD, int ROWS_>
 struct MmaTile {
-  static constexpr int ROWS = ROWS_;
+  static constexpr int ROWS = ROWS_, kKeys = 16;   // keys of a stage
   static constexpr int kSmem = 0;
   static constexpr bool k8 = sizeof(C) == 1;
   using M = typename std::conditional<k8, __half, T>::type;   // the products' type
@@ -141,6 +138,11 @@ struct MmaTile {
   static constexpr bool kSplit = !k8 || ROWS == 8;            // P as two numbers
   static_assert(ROWS == 8 || ROWS == 16, "");
   static_assert(VI >= 1 && KJ == 2 * VI, "");
+
+  // Rows of a stage lie one behind the other; the 16-byte pieces of a row are permuted within groups of
+  // eight so that the fragment reads below meet every bank once: K's quarter-warps read the same pieces of two
+  // neighbouring rows, V's two neighbouring pieces of rows 4 apart.
+  static __device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) ^ (((row >> 2) & 3) << 1); }
 
   uint32_t q[KJ][ROWS / 8][QW], next[KJ][ROWS / 8][QW];
   float o[VI][DC][4];
@@ -385,127 +387,177 @@ struct MmaTile {
 };
 
 // ---------------------------------------------------------------------------------------------
-// The same in fp32 on CUDA cores: a lane pair per key for the scores, a lane per four columns for o.
+// The same for fp32.
 // ---------------------------------------------------------------------------------------------
+// x = hi + lo, hi rounded to the 11 bits of tf32; of lo's 12 bits and a sign the product takes the leading
+// 11, so what is lost is at most 2^-23 of x's leading bit.
+struct Split {
+  uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ Split split4(uint4 u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  Split s;
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s.hi[i] = (w[i] + 0x1000u) & 0xFFFFE000u;
+    s.lo[i] = __float_as_uint(__uint_as_float(w[i]) - __uint_as_float(s.hi[i]));
+    mx = fmaxf(mx, fabsf(__uint_as_float(w[i])));
+  }
+  if (mx > 3.4e38f) {   // hi may not be rounded up to an infinity, and an infinity has no lower part
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s.hi[i] = w[i] & 0xFFFFE000u;
+      s.lo[i] = (w[i] & 0x7FFFFFFFu) == 0x7F800000u ? 0u : __float_as_uint(__uint_as_float(w[i]) - __uint_as_float(s.hi[i]));
+    }
+  }
+  return s;
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 template <int HD>
-struct SimtTile {
-  static constexpr int ROWS = 8;
-  static constexpr bool kAhead = false;
+struct Tf32Tile {
+  static constexpr int ROWS = 8, kKeys = 8;
   static constexpr int RB = HD * 4;
-  static constexpr int CB = HD > 128 ? HD / 128 : 1;          // float4 columns per lane
-  static constexpr int kSmem = (ROWS * HD + ROWS * kKeys) * 4;   // q and p of a warp
+  static constexpr int KJ = HD / 16, VI = HD / 32;
+  static constexpr bool kAhead = false;
+  static constexpr bool kQueryInSmem = HD > 128;   // the registers do not hold it beside o
+  static constexpr int kSmem = kQueryInSmem ? ROWS * HD * 4 : 0;
 
-  float o[ROWS][CB][4];
-  float m[ROWS], l[ROWS], sc;
-  int rows;
+  uint32_t qh[kQueryInSmem ? 1 : KJ][4], ql[kQueryInSmem ? 1 : KJ][4];
+  float o[VI][4][4];
+  float m, l, sc;
 
-  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows_, float scale, int lane, float* sm) {
-    rows = rows_;
+  // K's quarter-warps read the same pieces of two neighbouring rows, V's two neighbouring pieces of rows 2 apart.
+  static __device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) ^ (((row >> 1) & 3) << 1); }
+
+  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float* sm) {
+    const int r = lane >> 2, c = lane & 3;
+    const float* src = (const float*)p.a.q + n * p.a.q_token + (row0 + r) * p.a.q_head;
+    if constexpr (kQueryInSmem) __syncwarp();
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+      const int e = (c + 4 * j) * 4;
+      const uint4 u = r < rows && e < p.a.E ? *(const uint4*)(src + e) : make_uint4(0, 0, 0, 0);
+      if constexpr (kQueryInSmem) {
+        *(uint4*)(sm + r * HD + (((c + 4 * j) ^ ((r & 1) << 2)) << 2)) = u;
+      } else {
+        const Split s = split4(u);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          qh[j][y] = s.hi[y];
+          ql[j][y] = s.lo[y];
+        }
+      }
+    }
+    if constexpr (kQueryInSmem) __syncwarp();
     sc = scale;
-    __syncwarp();
-    for (int g = 0; g < rows; ++g) {
-      const float* src = (const float*)p.a.q + n * p.a.q_token + (row0 + g) * p.a.q_head;
-      for (int e = lane * 4; e < HD; e += 128)
-        *(float4*)(sm + g * HD + e) = e < p.a.E ? *(const float4*)(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __syncwarp();
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
-    for (int g = 0; g < ROWS; ++g) {
-      m[g] = -INFINITY;
-      l[g] = 0.f;
+    for (int i = 0; i < VI; ++i)
 #pragma unroll
-      for (int x = 0; x < CB; ++x) o[g][x][0] = o[g][x][1] = o[g][x][2] = o[g][x][3] = 0.f;
-    }
+      for (int y = 0; y < 4; ++y) o[i][y][0] = o[i][y][1] = o[i][y][2] = o[i][y][3] = 0.f;
   }
 
   __device__ __forceinline__ void step(const PagedAttn& p, uint32_t ks, uint32_t vs, uint32_t seen, int lane, float* sm) {
-    // lanes 2 j and 2 j + 1 of a quarter-warp take the even and odd pieces of one key's row
-    const int half = lane & 1, key = 4 * ((lane >> 1) & 3) + (lane >> 3);
-    float z[ROWS];
+    const int r = lane >> 2, c = lane & 3;
+    float s0[4] = {}, s1[4] = {};
+    const uint32_t ka = ks + r * RB + ((c ^ swizzle(r)) << 4);   // column r of S is key r
 #pragma unroll
-    for (int g = 0; g < ROWS; ++g) z[g] = 0.f;
-    const int pieces = (p.a.E + 3) / 4;
-    for (int i = half; i < pieces; i += 2) {
-      const uint4 u = lds16(ks + key * RB + ((i ^ swizzle(key)) << 4));
-      const float k0 = __uint_as_float(u.x), k1 = __uint_as_float(u.y), k2 = __uint_as_float(u.z), k3 = __uint_as_float(u.w);
+    for (int j = 0; j < KJ; ++j) {
+      if (j * 16 >= p.a.E) break;
+      const Split k = split4(lds16((ka ^ ((j & 1) << 6)) + (j >> 1) * 128));
+      uint32_t h[4], w[4];
+      if constexpr (kQueryInSmem) {
+        const Split q = split4(*(const uint4*)(sm + r * HD + (((c + 4 * j) ^ ((r & 1) << 2)) << 2)));
 #pragma unroll
-      for (int g = 0; g < ROWS; ++g) {
-        if (g >= rows) break;
-        const float4 q = *(const float4*)(sm + g * HD + 4 * i);
-        z[g] = fmaf(q.x, k0, z[g]);
-        z[g] = fmaf(q.y, k1, z[g]);
-        z[g] = fmaf(q.z, k2, z[g]);
-        z[g] = fmaf(q.w, k3, z[g]);
-      }
-    }
-    const bool on = (seen >> key) & 1;
-    float* ps = sm + ROWS * HD;
-    __syncwarp();
-#pragma unroll
-    for (int g = 0; g < ROWS; ++g) {
-      if (g >= rows) break;
-      float x = z[g] + __shfl_xor_sync(0xffffffffu, z[g], 1);
-      x = on ? x * sc : -INFINITY;
-      float mx = x;
-#pragma unroll
-      for (int o_ = 2; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o_));
-      const float mn = fmaxf(m[g], mx), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m[g] - ref);
-      m[g] = mn;
-      const float w = ex2(x - ref);
-      l[g] = l[g] * f + (half ? 0.f : w);
-      if (!half) ps[g * kKeys + key] = w;
-#pragma unroll
-      for (int x2 = 0; x2 < CB; ++x2)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[g][x2][y] *= f;
-    }
-    __syncwarp();
-    for (int j = 0; j < kKeys; j += 4) {
-      float4 w[ROWS];
-#pragma unroll
-      for (int g = 0; g < ROWS; ++g)
-        if (g < rows) w[g] = *(const float4*)(ps + g * kKeys + j);
-#pragma unroll
-      for (int x = 0; x < CB; ++x) {
-        const int d = lane + 32 * x;   // float4 column
-        if (4 * d >= p.a.D) break;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 u = lds16(vs + (j + k) * RB + ((d ^ swizzle(j + k)) << 4));
-          const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-#pragma unroll
-          for (int g = 0; g < ROWS; ++g) {
-            if (g >= rows) break;
-            const float pw = k == 0 ? w[g].x : k == 1 ? w[g].y : k == 2 ? w[g].z : w[g].w;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) o[g][x][y] = fmaf(pw, v[y], o[g][x][y]);
-          }
+        for (int y = 0; y < 4; ++y) {
+          h[y] = q.hi[y];
+          w[y] = q.lo[y];
         }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          h[y] = qh[j][y];
+          w[y] = ql[j][y];
+        }
+      }
+      const uint32_t a0[4] = {h[0], w[0], h[1], w[1]}, a1[4] = {h[2], w[2], h[3], w[3]};
+      mma_tf32(s0, a0, k.hi[0], k.hi[1]);
+      mma_tf32(s1, a0, k.lo[0], k.lo[1]);
+      mma_tf32(s0, a1, k.hi[2], k.hi[3]);
+      mma_tf32(s1, a1, k.lo[2], k.lo[3]);
+    }
+    // row r against keys 2 c and 2 c + 1; z is rounded before the maximum is taken, so that z - m is 0 at
+    // the maximum, however large both are
+    float z[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      z[u] = (s0[u] + (s0[2 + u] + (s1[u] + s1[2 + u]))) * sc;
+      if (!((seen >> (2 * c + u)) & 1)) z[u] = -INFINITY;
+    }
+    float mx = fmaxf(z[0], z[1]);
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+    if (__any_sync(0xffffffffu, mn != m)) {
+      const float f = ex2(m - ref);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < VI; ++i)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          o[i][y][0] *= f;
+          o[i][y][1] *= f;
+          o[i][y][2] *= f;
+          o[i][y][3] *= f;
+        }
+    }
+    m = mn;
+    const float p0 = ex2(z[0] - ref), p1 = ex2(z[1] - ref);
+    l += p0 + p1;
+    const uint32_t h0 = __float_as_uint(p0) & 0xFFFFE000u, h1 = __float_as_uint(p1) & 0xFFFFE000u;
+    // P's slots c and c + 4 are keys 2 c and 2 c + 1
+    const uint32_t a[4] = {h0, __float_as_uint(p0 - __uint_as_float(h0)), h1, __float_as_uint(p1 - __uint_as_float(h1))};
+    const uint32_t va = vs + 2 * c * RB + ((r ^ (c << 1)) << 4);
+#pragma unroll
+    for (int i = 0; i < VI; ++i) {
+      if (i * 32 >= p.a.D) break;
+      const Split v0 = split4(lds16(va + i * 128)), v1 = split4(lds16((va ^ 64) + RB + i * 128));
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        mma_tf32(o[i][y], a, v0.hi[y], v1.hi[y]);
+        mma_tf32(o[i][y], a, v0.lo[y], v1.lo[y]);
       }
     }
   }
 
   __device__ __forceinline__ void finish(float* ml, int lane) {
-#pragma unroll
-    for (int g = 0; g < ROWS; ++g) {
-#pragma unroll
-      for (int o_ = 1; o_ < 32; o_ <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], o_);
-      if (lane == 0) {
-        ml[2 * g] = m[g];
-        ml[2 * g + 1] = l[g];
-      }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if ((lane & 3) == 0) {
+      ml[2 * (lane >> 2)] = m;
+      ml[2 * (lane >> 2) + 1] = l;
     }
   }
   static constexpr int COLS = HD > 64 ? 128 : 64;
-  static __device__ __forceinline__ int place(int g, int col) { return g * (COLS / 4) + col; }
+  static __device__ __forceinline__ int place(int g, int col) { return g * (COLS / 4) + (col ^ (g & 1)); }
   __device__ __forceinline__ void put(float4* dst, int part, int lane) {
+    const int r = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int x = 0; x < CB; ++x) {
-      const int d = 4 * (lane + 32 * x);
-      if (d >= HD || d / COLS != part) continue;
+    for (int i = 0; i < VI; ++i)
 #pragma unroll
-      for (int g = 0; g < ROWS; ++g) dst[place(g, d % COLS / 4)] = make_float4(o[g][x][0], o[g][x][1], o[g][x][2], o[g][x][3]);
-    }
+      for (int u = 0; u < 2; ++u) {
+        const int d = 4 * (2 * c + u + 8 * i);
+        if (d / COLS != part) continue;
+        dst[place(r, d % COLS / 4)] = make_float4(o[i][0][u] + o[i][0][2 + u], o[i][1][u] + o[i][1][2 + u],
+                                                  o[i][2][u] + o[i][2][2 + u], o[i][3][u] + o[i][3][2 + u]);
+      }
   }
 };
 
@@ -522,14 +574,14 @@ struct Parts {
 // A stage's place in the line, written by the warp that fills it.
 struct alignas(16) Meta {
   int n, tile;
-  uint32_t seen;   // bits 0..15, 16: first unit of a pair (here), 17: last unit (here)
+  uint32_t seen;   // a bit per key, 16: first unit of a pair (here), 17: last unit (here)
   int left;        // units of the pair behind it
 };
 
 template <typename Tile, typename C, int HD, int WARPS, int STAGES>
 struct Shape {
-  static constexpr int kUnit = WARPS * kKeys;
-  static constexpr int kStage = 2 * kKeys * HD * (int)sizeof(C);
+  static constexpr int kUnit = WARPS * Tile::kKeys;
+  static constexpr int kStage = 2 * Tile::kKeys * HD * (int)sizeof(C);
   static constexpr int kRing = WARPS * STAGES * kStage;
   static constexpr int kMerge = WARPS * Tile::ROWS * Tile::COLS * 4;
   static constexpr int kSmem = kRing + kMerge + WARPS * Tile::kSmem;
@@ -548,7 +600,8 @@ constexpr int kPairCost = 2;
 template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES, int PER_SM>
 __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn p, Parts parts) {
   using S = Shape<Tile, C, HD, WARPS, STAGES>;
-  constexpr int ROWS = Tile::ROWS, RB = HD * (int)sizeof(C), kThreads = WARPS * 32;
+  constexpr int ROWS = Tile::ROWS, RB = HD * (int)sizeof(C), kThreads = WARPS * 32, kKeys = Tile::kKeys;
+  constexpr uint32_t kAll = (1u << kKeys) - 1;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t sums[WARPS];
   __shared__ End ends_s[2];
@@ -650,7 +703,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
   bool on = false;
   // the page id of this lane's key at the filling side's place
   auto look = [&]() {
-    const int key = (tok.start & ~(kKeys - 1)) + unit * S::kUnit + warp * kKeys + row_key;
+    const int key = (tok.start & ~(kAlign - 1)) + unit * S::kUnit + warp * kKeys + row_key;
     on = key >= tok.start && key < tok.len;
     const int j = page_of(p, key);
     off = key - j * a.page;
@@ -669,17 +722,17 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
     if (more) {
       const int st = filled % STAGES;
       const bool held = id >= 0 && id < a.n_pages;
-      const uint32_t seen = __ballot_sync(0xffffffffu, on && held) & 0xFFFF;
+      const uint32_t seen = __ballot_sync(0xffffffffu, on && held) & kAll;
       const uint32_t ks = ring + st * S::kStage;
       const int64_t page = held ? id : 0;
-      if (whole && seen == 0xFFFF) {
+      if (whole && seen == kAll) {
         // sixteen rows a fixed stride apart
         const C* kr = k_head + page * a.kp_page + (off - row_key + r0) * a.kp_row + piece * (16 / (int)sizeof(C));
         const C* vr = v_head + page * a.vp_page + (off - row_key + r0) * a.vp_row + piece * (16 / (int)sizeof(C));
 #pragma unroll
         for (int i = 0; i < kKeys / RPI; ++i) {
           const int row = i * RPI;   // swizzle(row + r0) = swizzle(row) ^ ((r0 & 1) << 2)
-          const uint32_t at = ks + row * RB + (lane_at ^ (swizzle(row) << 4));
+          const uint32_t at = ks + row * RB + (lane_at ^ (Tile::swizzle(row) << 4));
 #pragma unroll
           for (int x = 0; x < CH; x += LPR) {
             if (piece + x < k_pieces) cp16(at + x * 16, (const char*)kr + x * 16);
@@ -695,7 +748,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
           const int row = i * RPI + r0;
           const bool full = (seen >> row) & 1;
           const C *kr = k_head + __shfl_sync(0xffffffffu, ko, row), *vr = v_head + __shfl_sync(0xffffffffu, vo, row);
-          const uint32_t at = ks + i * RPI * RB + (lane_at ^ (swizzle(i * RPI) << 4));
+          const uint32_t at = ks + i * RPI * RB + (lane_at ^ (Tile::swizzle(i * RPI) << 4));
 #pragma unroll
           for (int x = 0; x < CH; x += LPR) {
             if (piece + x < k_pieces) cp16(at + x * 16, full ? (const char*)kr + (piece + x) * 16 : (const char*)a.k_pages, full);
@@ -752,7 +805,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
     }
     if (s + 1 < filled && (meta[warp][(s + 1) % STAGES].seen >> 16 & 1)) fetch(meta[warp][(s + 1) % STAGES]);
     const uint32_t ks = ring + st * S::kStage;
-    if (me.seen & 0xFFFF) t.step(p, ks, ks + kKeys * RB, me.seen & 0xFFFF, lane, scratch);
+    if (me.seen & kAll) t.step(p, ks, ks + kKeys * RB, me.seen & kAll, lane, scratch);
     if (!(me.seen >> 17 & 1)) continue;
 
     // the pair's end in this CTA: join the warps, and finish the pair or leave a partial
@@ -925,16 +978,16 @@ cudaError_t launch_mma(const PagedAttn& p, void* ws, cudaStream_t st) {
     if (w <= 128) return launch_tile<MmaTile<T, e4m3, 128, ROWS>, T, e4m3, 128, 4, 3, 3>(p, ws, st);
     return launch_tile<MmaTile<T, e4m3, 256, ROWS>, T, e4m3, 256, 4, 3, 2>(p, ws, st);
   }
-  if (w <= 64) return launch_tile<MmaTile<T, T, 64, ROWS>, T, T, 64, 4, 5, 2>(p, ws, st);
+  if (w <= 64) return launch_tile<MmaTile<T, T, 64, ROWS>, T, T, 64, 4, ROWS == 8 ? 4 : 3, 3>(p, ws, st);
   if (w <= 128) return launch_tile<MmaTile<T, T, 128, ROWS>, T, T, 128, 4, 3, 2>(p, ws, st);
   return launch_tile<MmaTile<T, T, 256, ROWS>, T, T, 256, 4, 3, 1>(p, ws, st);
 }
 
-cudaError_t launch_simt(const PagedAttn& p, void* ws, cudaStream_t st) {
+cudaError_t launch_tf32(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int w = p.a.E > p.a.D ? p.a.E : p.a.D;
-  if (w <= 64) return launch_tile<SimtTile<64>, float, float, 64, 4, 2, 2>(p, ws, st);
-  if (w <= 128) return launch_tile<SimtTile<128>, float, float, 128, 4, 2, 1>(p, ws, st);
-  return launch_tile<SimtTile<256>, float, float, 256, 2, 2, 1>(p, ws, st);
+  if (w <= 64) return launch_tile<Tf32Tile<64>, float, float, 64, 4, 4, 3>(p, ws, st);
+  if (w <= 128) return launch_tile<Tf32Tile<128>, float, float, 128, 4, 3, 2>(p, ws, st);
+  return launch_tile<Tf32Tile<256>, float, float, 256, 4, 2, 1>(p, ws, st);
 }
 
 }  // namespace
@@ -942,7 +995,7 @@ cudaError_t launch_simt(const PagedAttn& p, void* ws, cudaStream_t st) {
 size_t paged_attention_workspace(const thin_attn_paged_attention_args& a) { return parts_layout(a).bytes; }
 
 cudaError_t launch_paged_attention(const PagedAttn& p, void* ws, cudaStream_t st) {
-  if (p.a.dtype == THIN_ATTN_FP32) return launch_simt(p, ws, st);
+  if (p.a.dtype == THIN_ATTN_FP32) return launch_tf32(p, ws, st);
   const bool few = rows_of(p.a) == 8;
   if (p.a.dtype == THIN_ATTN_BF16) return few ? launch_mma<__nv_bfloat16, 8>(p, ws, st) : launch_mma<__nv_bfloat16, 16>(p, ws, st);
   return few ? launch_mma<__half, 8>(p, ws, st) : launch_mma<__half, 16>(p, ws, st);
