@@ -426,7 +426,7 @@ struct Tf32Tile {
   static constexpr int KJ = HD / 16, VI = HD / 32;
   static constexpr bool kAhead = false;
   static constexpr bool kQueryInSmem = HD > 128;   // the registers do not hold it beside o
-  static constexpr int kSmem = kQueryInSmem ? ROWS * HD * 4 : 0;
+  static constexpr int kSmem = kQueryInSmem ? 2 * ROWS * HD * 4 : 0;   // of the CTA: its parts hi and lo
 
   uint32_t qh[kQueryInSmem ? 1 : KJ][4], ql[kQueryInSmem ? 1 : KJ][4];
   float o[VI][4][4];
@@ -435,18 +435,25 @@ struct Tf32Tile {
   // K's quarter-warps read the same pieces of two neighbouring rows, V's two neighbouring pieces of rows 2 apart.
   static __device__ __forceinline__ int swizzle(int row) { return ((row & 1) << 2) ^ (((row >> 1) & 3) << 1); }
 
+  // piece `col` of row r of the queries in shared memory, as an index of uint4
+  static __device__ __forceinline__ int query_at(int r, int col) { return r * (HD / 4) + (col ^ ((r & 1) << 2)); }
+
   __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float* sm) {
-    const int r = lane >> 2, c = lane & 3;
-    const float* src = (const float*)p.a.q + n * p.a.q_token + (row0 + r) * p.a.q_head;
-    if constexpr (kQueryInSmem) __syncwarp();
+    const float* src = (const float*)p.a.q + n * p.a.q_token + row0 * p.a.q_head;
+    if constexpr (kQueryInSmem) {   // for every thread of the CTA alike, and behind the last pair's join
+      for (int i = threadIdx.x; i < ROWS * HD / 4; i += blockDim.x) {
+        const int r = i / (HD / 4), col = i % (HD / 4);
+        const Split s = split4(r < rows && col * 4 < p.a.E ? *(const uint4*)(src + r * p.a.q_head + col * 4) : make_uint4(0, 0, 0, 0));
+        ((uint4*)sm)[query_at(r, col)] = make_uint4(s.hi[0], s.hi[1], s.hi[2], s.hi[3]);
+        ((uint4*)sm)[ROWS * HD / 4 + query_at(r, col)] = make_uint4(s.lo[0], s.lo[1], s.lo[2], s.lo[3]);
+      }
+      __syncthreads();
+    } else {
+      const int r = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      const int e = (c + 4 * j) * 4;
-      const uint4 u = r < rows && e < p.a.E ? *(const uint4*)(src + e) : make_uint4(0, 0, 0, 0);
-      if constexpr (kQueryInSmem) {
-        *(uint4*)(sm + r * HD + (((c + 4 * j) ^ ((r & 1) << 2)) << 2)) = u;
-      } else {
-        const Split s = split4(u);
+      for (int j = 0; j < KJ; ++j) {
+        const int e = (c + 4 * j) * 4;
+        const Split s = split4(r < rows && e < p.a.E ? *(const uint4*)(src + r * p.a.q_head + e) : make_uint4(0, 0, 0, 0));
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           qh[j][y] = s.hi[y];
@@ -454,7 +461,6 @@ struct Tf32Tile {
         }
       }
     }
-    if constexpr (kQueryInSmem) __syncwarp();
     sc = scale;
     m = -INFINITY;
     l = 0.f;
@@ -474,12 +480,15 @@ struct Tf32Tile {
       const Split k = split4(lds16((ka ^ ((j & 1) << 6)) + (j >> 1) * 128));
       uint32_t h[4], w[4];
       if constexpr (kQueryInSmem) {
-        const Split q = split4(*(const uint4*)(sm + r * HD + (((c + 4 * j) ^ ((r & 1) << 2)) << 2)));
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          h[y] = q.hi[y];
-          w[y] = q.lo[y];
-        }
+        const uint4 qa = ((const uint4*)sm)[query_at(r, c + 4 * j)], qb = ((const uint4*)sm)[ROWS * HD / 4 + query_at(r, c + 4 * j)];
+        h[0] = qa.x;
+        h[1] = qa.y;
+        h[2] = qa.z;
+        h[3] = qa.w;
+        w[0] = qb.x;
+        w[1] = qb.y;
+        w[2] = qb.z;
+        w[3] = qb.w;
       } else {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -545,7 +554,7 @@ struct Tf32Tile {
       ml[2 * (lane >> 2) + 1] = l;
     }
   }
-  static constexpr int COLS = HD > 64 ? 128 : 64;
+  static constexpr int COLS = HD == 128 ? 128 : 64;
   static __device__ __forceinline__ int place(int g, int col) { return g * (COLS / 4) + (col ^ (g & 1)); }
   __device__ __forceinline__ void put(float4* dst, int part, int lane) {
     const int r = lane >> 2, c = lane & 3;
@@ -584,7 +593,7 @@ struct Shape {
   static constexpr int kStage = 2 * Tile::kKeys * HD * (int)sizeof(C);
   static constexpr int kRing = WARPS * STAGES * kStage;
   static constexpr int kMerge = WARPS * Tile::ROWS * Tile::COLS * 4;
-  static constexpr int kSmem = kRing + kMerge + WARPS * Tile::kSmem;
+  static constexpr int kSmem = kRing + kMerge + Tile::kSmem;
 };
 
 // A place on the line.
@@ -682,7 +691,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
   auto ended = [&]() { return n > end.n || (n == end.n && (tile > end.tile || (tile == end.tile && unit > end.unit))); };
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * S::kStage;
   float4* const merge = (float4*)(smem + S::kRing);
-  float* const scratch = (float*)(smem + S::kRing + S::kMerge) + warp * (Tile::kSmem / 4);
+  float* const scratch = (float*)(smem + S::kRing + S::kMerge);
   if (a.E < HD) {
     // the columns behind E are never written again
     for (int i = lane; i < STAGES * S::kStage / 16; i += 32) *(uint4*)(smem + warp * STAGES * S::kStage + i * 16) = make_uint4(0, 0, 0, 0);
@@ -987,7 +996,7 @@ cudaError_t launch_tf32(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int w = p.a.E > p.a.D ? p.a.E : p.a.D;
   if (w <= 64) return launch_tile<Tf32Tile<64>, float, float, 64, 4, 4, 3>(p, ws, st);
   if (w <= 128) return launch_tile<Tf32Tile<128>, float, float, 128, 4, 3, 2>(p, ws, st);
-  return launch_tile<Tf32Tile<256>, float, float, 256, 4, 2, 1>(p, ws, st);
+  return launch_tile<Tf32Tile<256>, float, float, 256, 6, 2, 1>(p, ws, st);
 }
 
 }  // namespace
