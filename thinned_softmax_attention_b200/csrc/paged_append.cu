@@ -22,36 +22,72 @@ namespace thin {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMany = 64, kFew = 8;   // tokens of a block, at most
+constexpr int kMany = 64, kFew = 8;   // tokens of a block, at most and at least
 constexpr int kPieces = 4;            // pieces of keys that a thread copies
 constexpr int kShort = 16;            // tokens of a run that one warp takes
 
-// Eight elements of type T as a cache of type C holds them; e4m3: the quotient is rounded to fp32, then to e4m3.
+// x / scale by the rounded reciprocal and one correction of the remainder (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): the rounded quotient, one step of
+// fp32 off in about 1 of 10^8 pairs, which the rounding to 4 bits behind it does not see.  Divisions take three times
+// as long and would bound the kernel.  Very large quotients go uncorrected (they are clamped), scales of
+// unusual size by division.
+struct Quotient {
+  float scale, inverse;
+  bool plain;
+  __device__ __forceinline__ explicit Quotient(float s) : scale(s), inverse(1.f / s), plain(!(fabsf(s) > 1e-18f && fabsf(s) < 1e18f)) {}
+  __device__ __forceinline__ float operator()(float x) const {
+    const float q = x * inverse, better = fmaf(fmaf(-q, scale, x), inverse, q);
+    return fabsf(q) < 1048576.f ? better : q;
+  }
+};
+
+// Eight elements as they are given, and as a cache of type C holds them.
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* src) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ((const uint4*)src)[i];
+  }
+};
 template <typename C>
 struct Held {
   static constexpr int kWords = 2 * (int)sizeof(C);
   uint32_t w[kWords];
 };
+__device__ __noinline__ void divide8(float* x, float scale) {
+  for (int i = 0; i < 8; ++i) x[i] /= scale;
+}
 template <typename T, typename C>
-__device__ __forceinline__ Held<C> held_of(const T* src, float scale) {
+__device__ __forceinline__ Held<C> held_of(const Raw<T>& r, const Quotient& by) {
   Held<C> y;
   if constexpr (sizeof(C) == 1) {
     float x[8];
-    load8(src, x);
+    load8((const T*)r.w, x);
+    if (by.plain) {   // for the whole grid alike per head
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = x[i];
+      divide8(z, by.scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = z[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = by(x[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i] / scale, x[i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i + 2] / scale, x[i + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i], x[i + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i + 2], x[i + 3]), __NV_SATFINITE, __NV_E4M3);
       y.w[i / 4] = lo | hi << 16;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < Held<C>::kWords; i += 4) {
-      const uint4 u = ((const uint4*)src)[i / 4];
-      y.w[i] = u.x;
-      y.w[i + 1] = u.y;
-      y.w[i + 2] = u.z;
-      y.w[i + 3] = u.w;
+      y.w[i] = r.w[i / 4].x;
+      y.w[i + 1] = r.w[i / 4].y;
+      y.w[i + 2] = r.w[i / 4].z;
+      y.w[i + 3] = r.w[i / 4].w;
     }
   }
   return y;
@@ -160,10 +196,18 @@ struct Range {
 };
 // Over tokens first, first + step, ... below last.
 template <typename T, typename C>
-__device__ __forceinline__ void range_of(const thin_attn_paged_append_args& a, Range<C>& g, int first, int last, int step, int h, int col, float ks) {
+__device__ __forceinline__ void range_of(const thin_attn_paged_append_args& a, Range<C>& g, int first, int last, int step, int h, int col, const Quotient& ks) {
   const T* src = (const T*)a.k + h * a.k_head + col;
-#pragma unroll 4
-  for (int t = first; t < last; t += step) g.take(held_of<T, C>(src + t * a.k_token, ks));
+  constexpr int U = 4;
+  for (int t = first; t < last; t += U * step) {
+    Raw<T> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + u * step < last) x[u].load(src + (t + u * step) * a.k_token);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + u * step < last) g.take(held_of<T, C>(x[u], ks));
+  }
 }
 
 struct Stored {
@@ -213,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) append_kerne
   // k_shift, v_shift: 2^shift threads take a row, 8 elements each
   const int h = blockIdx.x % a.H, t0 = blockIdx.x / a.H * block, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ int page_s[kMany + 2], off_s[kMany];   // page_s[0]: the token before the block, [block + 1]: none
+  // the slots behind the block, for its last run's end
+  int64_t behind = a.bounds && t0 + block + lane < a.N ? a.slots[t0 + block + lane] : -1;
   if (tid <= block + 1) {
     const int t = t0 + tid - 1;
     const int64_t slot = t >= 0 && t < a.N && tid <= block ? a.slots[t] : -1;
@@ -224,31 +270,42 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) append_kerne
     page_s[tid] = pg;
   }
   __syncthreads();
-  const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
+  if (a.bounds && tid < block && page_s[tid + 1] >= 0 && page_s[tid + 1] != page_s[tid]) {
+    // a run's stored bounds, wanted when its keys have been read
+    const int64_t at = (int64_t)page_s[tid + 1] * a.H + h;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.exps + at));
+    for (int i = 0; i < 2 * a.E; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.bounds + at * 2 * a.E + i));
+  }
+  const Quotient ks(a.k_scale ? a.k_scale[h] : 1.f), vs(a.v_scale ? a.v_scale[h] : 1.f);
   const int k_col = (tid & ((1 << k_shift) - 1)) * 8, v_col = (tid & ((1 << v_shift) - 1)) * 8;
   const int k_row = tid >> k_shift, v_row = tid >> v_shift, k_step = kThreads >> k_shift, v_step = kThreads >> v_shift;
-  Held<C> x[kPieces];
-  // the host chose the block so that kPieces turns cover its keys
-  bool has[kPieces];
-#pragma unroll
-  for (int u = 0; u < kPieces; ++u) {
-    const int r = k_row + u * k_step;
-    has[u] = r < block && k_col < a.E && page_s[r + 1] >= 0;
-    if (has[u]) x[u] = held_of<T, C>((const T*)a.k + (t0 + r) * a.k_token + h * a.k_head + k_col, ks);
-  }
   for (int r0 = v_row; r0 < block; r0 += kPieces * v_step) {
-    Held<C> y[kPieces];
+    Raw<T> raw[kPieces];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int r = r0 + u * v_step;
-      if (r < block && v_col < a.D && page_s[r + 1] >= 0) y[u] = held_of<T, C>((const T*)a.v + (t0 + r) * a.v_token + h * a.v_head + v_col, vs);
+      if (r < block && v_col < a.D && page_s[r + 1] >= 0) raw[u].load((const T*)a.v + (t0 + r) * a.v_token + h * a.v_head + v_col);
     }
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int r = r0 + u * v_step;
       if (r < block && v_col < a.D && page_s[r + 1] >= 0)
-        put_held((C*)a.v_pages + page_s[r + 1] * a.vp_page + h * a.vp_head + off_s[r] * a.vp_row + v_col, y[u]);
+        put_held((C*)a.v_pages + page_s[r + 1] * a.vp_page + h * a.vp_head + off_s[r] * a.vp_row + v_col, held_of<T, C>(raw[u], vs));
     }
+  }
+  // the host chose the block so that kPieces turns cover its keys
+  Held<C> x[kPieces];
+  bool has[kPieces];
+  {
+    Raw<T> raw[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int r = k_row + u * k_step;
+      has[u] = r < block && k_col < a.E && page_s[r + 1] >= 0;
+      if (has[u]) raw[u].load((const T*)a.k + (t0 + r) * a.k_token + h * a.k_head + k_col);
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) x[u] = held_of<T, C>(raw[u], ks);
   }
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
@@ -262,16 +319,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) append_kerne
   bool tail_anew = false;
   if (page_s[block] >= 0) {
     const int64_t begin = (int64_t)page_s[block] * a.page;
-    for (;; tail += 32) {
-      const int t = t0 + block + tail + lane;
-      const int64_t slot = t < a.N ? a.slots[t] : -1;
-      const uint32_t in = __ballot_sync(0xffffffffu, slot >= begin && slot < begin + a.page);
+    for (;;) {
+      const uint32_t in = __ballot_sync(0xffffffffu, behind >= begin && behind < begin + a.page);
       const int run = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-      tail_anew |= __any_sync(0xffffffffu, lane < run && slot == begin);
-      if (run < 32) {
-        tail += run;
-        break;
-      }
+      tail_anew |= __any_sync(0xffffffffu, lane < run && behind == begin);
+      tail += run;
+      if (run < 32) break;
+      const int t = t0 + block + tail + lane;
+      behind = t < a.N ? a.slots[t] : -1;
     }
   }
   // of the runs that begin in a block all but the last end in it: at most four of 64 tokens have more than
@@ -366,11 +421,11 @@ int shift_of(int width) {
 template <typename T, typename C>
 cudaError_t launch_t(const thin_attn_paged_append_args& a, cudaStream_t st) {
   const int k_shift = shift_of(a.E), v_shift = shift_of(a.D);
-  // as many tokens as kPieces turns cover, where such blocks fill the GPU; few for a decode step's
-  // tokens, one page each
+  // as many tokens as kPieces turns cover, fewer where the blocks would not fill the GPU: a decode step's
+  // tokens, one page each, are spread over more CTAs
   int block = kPieces * kThreads >> k_shift;
   if (block > kMany) block = kMany;
-  if ((int64_t)a.N * a.H < 148 * kMany) block = kFew;
+  while (block > kFew && (int64_t)((a.N + block - 1) / block) * a.H < 148 * 4) block /= 2;
   const int64_t grid = (int64_t)((a.N + block - 1) / block) * a.H;
   append_kernel<T, C><<<(unsigned)grid, kThreads, 0, st>>>(a, block, k_shift, v_shift);
   return cudaGetLastError();
