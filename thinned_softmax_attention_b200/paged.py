@@ -30,6 +30,7 @@ _APPEND = struct.Struct("@I9iPqqPqqPPqqqPqqqPPPP")
 _ATTENTION = struct.Struct("@I16ifPqqPqqqPqqqPqPPPPPPPPqqPPN")
 
 _fns = None
+_empty = torch.empty_strided   # half the time of torch.empty for more than one dimension
 _stream = torch._C._cuda_getCurrentRawStream   # of a device ordinal; what current_stream(...).cuda_stream reads
 
 
@@ -154,9 +155,9 @@ def paged_plan(lengths: torch.Tensor, new: torch.Tensor, table: torch.Tensor, fr
         raise ValueError(f"table of {rows_} rows, {R} requests, page={page}, max_tokens={T}: expected a row per request, page >= 1, "
                          "max_tokens >= 0")
     device = lengths.device
-    slots = torch.empty(T, dtype=torch.int64, device=device)
+    slots = _empty((T,), (1,), dtype=torch.int64, device=device)
     sizes = (T, T, R + 1, R) if inplace else (T, T, R + 1, R, R, 1)
-    parts = torch.split_with_sizes(torch.empty(sum(sizes), dtype=i32, device=device), sizes)   # one allocation
+    parts = torch.unsafe_split_with_sizes(_empty((sum(sizes),), (1,), dtype=i32, device=device), sizes)   # one allocation
     rows, context, cu, status = parts[:4]
     lengths_out, n_free_out = (lengths, n_free) if inplace else parts[4:]
     p = _PLAN.pack(_PLAN.size, dev, R, W, page, n_pages, T, 0, *at, table.data_ptr(), row, *pool, lengths_out.data_ptr(),
@@ -236,26 +237,30 @@ def _attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scal
     ks, vs = _scales(k_scale, v_scale, ct, H, dev)
     device = q.device
     # rows of padding tokens are not written: zeros there where the buffer is made here
-    make = torch.empty if rows is None else torch.zeros
     if out is None:
-        out = torch.empty_like(q) if rows is None and D == E and q.is_contiguous() else make((N, Hq, D), dtype=q.dtype, device=device)
+        out = _empty((N, Hq, D), (Hq * D, D, 1), dtype=q.dtype, device=device)
+        if rows is not None:
+            out.zero_()
     ost = out.stride()
     if out.shape != (N, Hq, D) or out.dtype is not q.dtype or out.get_device() != dev or ost[2] != 1:
         raise ValueError(f"out: expected {q.dtype} {(N, Hq, D)} with a contiguous last axis on cuda:{dev}, got {_place(out)}")
     if lse is None:
         if return_lse:
-            lse = make((N, Hq), dtype=torch.float32, device=device)
+            lse = _empty((N, Hq), (Hq, 1), dtype=torch.float32, device=device)
+            if rows is not None:
+                lse.zero_()
     elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError(f"lse: expected contiguous float32 {(N, Hq)} on cuda:{dev}, got {_place(lse)}")
     b, x = (0, 0) if bounds is None else _bounds(bounds, P, H, E, dev)
     pages = None
     if return_pages:
-        pages = torch.empty((N, H, top), dtype=torch.int32, device=device) if rows is None else torch.full(
-            (N, H, top), -1, dtype=torch.int32, device=device)
+        pages = _empty((N, H, top), (H * top, top, 1), dtype=torch.int32, device=device)
+        if rows is not None:
+            pages.fill_(-1)
     n = _workspace_bytes(dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last, rows is not None)
     # scratch of this call alone: the caching allocator hands it on in stream order, and a capture
     # gets its own from the graph's pool
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = _empty((n,), (1,), dtype=torch.uint8, device=device)
     p = _ATTENTION.pack(_ATTENTION.size, dev, dt, ct, N, R, W, Hq, H, E, D, page, P, window, top, first, last,
                         0.0 if scale is None else scale, q.data_ptr(), qst[0], qst[1], k_pages.data_ptr(), kt[0], kt[1], kt[2],
                         v_pages.data_ptr(), vt[0], vt[1], vt[2], table.data_ptr(), row, seen, of, ks, vs, b, x,
