@@ -36,7 +36,7 @@ namespace thin {
 
 namespace {
 
-constexpr int kAlign = 16;         // keys before a window that its first stage may hold
+constexpr int kAlign = 32;         // keys before a window that its first stage may hold, a multiple of a stage's
 constexpr int kMaxCtas = 444;      // 148 SMs x 3
 
 // One token of the call: its row of outputs, its visible keys [start, len) and their units.
@@ -127,7 +127,7 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 // ---------------------------------------------------------------------------------------------
 template <typename T, typename C, int HD, int ROWS_>
 struct MmaTile {
-  static constexpr int ROWS = ROWS_, kKeys = 16;   // keys of a stage
+  static constexpr int ROWS = ROWS_;
   static constexpr int kSmem = 0;
   static constexpr bool k8 = sizeof(C) == 1;
   using M = typename std::conditional<k8, __half, T>::type;   // the products' type
@@ -136,6 +136,8 @@ struct MmaTile {
   static constexpr int KJ = RB / 64, VI = RB / 128;           // pieces of K and V per lane and row
   static constexpr int QW = DC / 2;                           // words of Q per piece
   static constexpr bool kSplit = !k8 || ROWS == 8;            // P as two numbers
+  static constexpr int kKeys = RB <= 128 ? 32 : 16;           // keys of a stage: short rows, twice as many for the same overhead
+  static constexpr int NB = kKeys / 16;                       // products' blocks of 16 keys
   static_assert(ROWS == 8 || ROWS == 16, "");
   static_assert(VI >= 1 && KJ == 2 * VI, "");
 
@@ -217,16 +219,16 @@ struct MmaTile {
   // One stage: keys at smem address ks, values at vs; bit j of `seen` is key j's.
   __device__ __forceinline__ void step(const PagedAttn& p, uint32_t ks, uint32_t vs, uint32_t seen, int lane, float*) {
     const int r = lane >> 2, c = lane & 3;
-    float s[2][4] = {}, s2[2][4] = {};   // two chains per tile, for the products' latency
+    float s[NB][2][4] = {}, s2[NB][2][4] = {};   // two chains per tile, for the products' latency
     const uint32_t zero = 0;
-    // column r of S's tile t is key 4 (r >> 1) + 2 t + (r & 1)
+    // column r of S's tile t is key 4 (r >> 1) + 2 t + (r & 1) of a block
     const uint32_t ka = ks + (4 * (r >> 1) + (r & 1)) * RB + ((c ^ swizzle(4 * (r >> 1) + (r & 1))) << 4);
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
       if (j * 4 * DC >= p.a.E) break;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint4 u = lds16((ka ^ ((j & 1) << 6)) + 2 * t * RB + (j >> 1) * 128);
+      for (int t = 0; t < 2 * NB; ++t) {
+        const uint4 u = lds16((ka ^ ((j & 1) << 6)) + ((t >> 1) * 16 + 2 * (t & 1)) * RB + (j >> 1) * 128);
         uint32_t b[QW];
         if constexpr (k8) {
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -242,36 +244,39 @@ struct MmaTile {
         for (int y = 0; y < QW; y += 2) {
           const uint32_t a[4] = {q[j][0][y], ROWS == 16 ? q[j][ROWS / 8 - 1][y] : zero, q[j][0][y + 1],
                                  ROWS == 16 ? q[j][ROWS / 8 - 1][y + 1] : zero};
-          mma<M>(y & 2 ? s2[t] : s[t], a, b[y], b[y + 1]);
+          mma<M>(y & 2 ? s2[t >> 1][t & 1] : s[t >> 1][t & 1], a, b[y], b[y + 1]);
         }
       }
     }
+    // s[b][t][2 x + u] = row r + 8 x against key 16 b + 4 c + 2 t + u; z is rounded before the maximum is taken,
+    // so that z - m is 0 at the maximum, however large both are
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) s[t][x] += s2[t][x];
-    // s[t][2 x + u] = row r + 8 x against key 4 c + 2 t + u
-    // z is rounded before the maximum is taken, so that z - m is 0 at the maximum, however large both are
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int x = 0; x < ROWS / 8; ++x) {
-        s[t][2 * x] *= sc[x];
-        s[t][2 * x + 1] *= sc[x];
-      }
-    if (seen != 0xFFFF) {
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (!((seen >> (4 * c + 2 * t + u)) & 1)) s[t][u] = s[t][2 + u] = -INFINITY;
+        for (int x = 0; x < ROWS / 8; ++x) {
+          s[b][t][2 * x] = (s[b][t][2 * x] + s2[b][t][2 * x]) * sc[x];
+          s[b][t][2 * x + 1] = (s[b][t][2 * x + 1] + s2[b][t][2 * x + 1]) * sc[x];
+        }
+    if (seen != (kKeys == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (!((seen >> (16 * b + 4 * c + 2 * t + u)) & 1)) s[b][t][u] = s[b][t][2 + u] = -INFINITY;
     }
-    uint32_t hi[2][2], lo[2][2];   // [x][t]
+    uint32_t hi[2][NB][2], lo[2][NB][2];   // [x][b][t]
     float f[2];
     bool grown = false;
 #pragma unroll
     for (int x = 0; x < ROWS / 8; ++x) {
-      float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+      float mx = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        mx = fmaxf(mx, fmaxf(fmaxf(s[b][0][2 * x], s[b][0][2 * x + 1]), fmaxf(s[b][1][2 * x], s[b][1][2 * x + 1])));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float mn = fmaxf(m[x], mx);
@@ -281,15 +286,17 @@ struct MmaTile {
       m[x] = mn;
       float sum = 0.f;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float a = ex2(s[t][2 * x] - ref), b = ex2(s[t][2 * x + 1] - ref);
-        sum += a + b;
-        hi[x][t] = pack2<M>(a, b);
-        if constexpr (kSplit) {
-          const float2 h = unpack2<M>(hi[x][t]);
-          lo[x][t] = pack2<M>(a - h.x, b - h.y);
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = ex2(s[b][t][2 * x] - ref), p1 = ex2(s[b][t][2 * x + 1] - ref);
+          sum += p0 + p1;
+          hi[x][b][t] = pack2<M>(p0, p1);
+          if constexpr (kSplit) {
+            const float2 h = unpack2<M>(hi[x][b][t]);
+            lo[x][b][t] = pack2<M>(p0 - h.x, p1 - h.y);
+          }
         }
-      }
       l[x] = l[x] * f[x] + sum;
     }
     if (__any_sync(0xffffffffu, grown)) {
@@ -304,42 +311,46 @@ struct MmaTile {
           o[i][y][3] *= f1;
         }
     }
-    uint32_t a[4] = {hi[0][0], ROWS == 16 ? hi[ROWS / 8 - 1][0] : lo[0][0], hi[0][1], ROWS == 16 ? hi[ROWS / 8 - 1][1] : lo[0][1]};
-    uint32_t a2[4] = {lo[0][0], lo[ROWS / 8 - 1][0], lo[0][1], lo[ROWS / 8 - 1][1]};
     const uint32_t va = vs + 4 * c * RB + ((r ^ (c << 1)) << 4);
 #pragma unroll
-    for (int i = 0; i < VI; ++i) {
-      if (i * 8 * DC >= p.a.D) break;
-      uint32_t v[4][4];
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t a[4] = {hi[0][b][0], ROWS == 16 ? hi[ROWS / 8 - 1][b][0] : lo[0][b][0], hi[0][b][1],
+                             ROWS == 16 ? hi[ROWS / 8 - 1][b][1] : lo[0][b][1]};
+      const uint32_t a2[4] = {lo[0][b][0], lo[ROWS / 8 - 1][b][0], lo[0][b][1], lo[ROWS / 8 - 1][b][1]};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint4 u = lds16((va ^ ((k & 1) << 6)) + k * RB + i * 128);   // swizzle(4 c + k) = 4 (k & 1) ^ 2 c
-        v[k][0] = u.x;
-        v[k][1] = u.y;
-        v[k][2] = u.z;
-        v[k][3] = u.w;
-      }
+      for (int i = 0; i < VI; ++i) {
+        if (i * 8 * DC >= p.a.D) break;
+        uint32_t v[4][4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if constexpr (k8) {
+        for (int k = 0; k < 4; ++k) {
+          const uint4 u = lds16((va ^ ((k & 1) << 6)) + (16 * b + k) * RB + i * 128);   // swizzle(4 c + k) = 4 (k & 1) ^ 2 c
+          v[k][0] = u.x;
+          v[k][1] = u.y;
+          v[k][2] = u.z;
+          v[k][3] = u.w;
+        }
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            // bytes 2 y and 2 y + 1 of the word, those of two keys side by side
-            const uint32_t b0 = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
-            const uint32_t b1 = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
-            uint32_t p0[2], p1[2];
-            widen4(b0, p0[0], p0[1]);
-            widen4(b1, p1[0], p1[1]);
-            mma<M>(o[i][4 * w + 2 * y], a, p0[0], p1[0]);
-            mma<M>(o[i][4 * w + 2 * y + 1], a, p0[1], p1[1]);
-          }
-        } else {
+        for (int w = 0; w < 4; ++w) {
+          if constexpr (k8) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t sel = y ? 0x7632 : 0x5410;
-            const uint32_t b0 = __byte_perm(v[0][w], v[1][w], sel), b1 = __byte_perm(v[2][w], v[3][w], sel);
-            mma<M>(o[i][2 * w + y], a, b0, b1);
-            if constexpr (kSplit && ROWS == 16) mma<M>(o[i][2 * w + y], a2, b0, b1);
+            for (int y = 0; y < 2; ++y) {
+              // bytes 2 y and 2 y + 1 of the word, those of two keys side by side
+              const uint32_t b0 = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+              const uint32_t b1 = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+              uint32_t p0[2], p1[2];
+              widen4(b0, p0[0], p0[1]);
+              widen4(b1, p1[0], p1[1]);
+              mma<M>(o[i][4 * w + 2 * y], a, p0[0], p1[0]);
+              mma<M>(o[i][4 * w + 2 * y + 1], a, p0[1], p1[1]);
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t sel = y ? 0x7632 : 0x5410;
+              const uint32_t b0 = __byte_perm(v[0][w], v[1][w], sel), b1 = __byte_perm(v[2][w], v[3][w], sel);
+              mma<M>(o[i][2 * w + y], a, b0, b1);
+              if constexpr (kSplit && ROWS == 16) mma<M>(o[i][2 * w + y], a2, b0, b1);
+            }
           }
         }
       }
@@ -582,9 +593,12 @@ struct Parts {
 
 // A stage's place in the line, written by the warp that fills it.
 struct alignas(16) Meta {
-  int n, tile;
-  uint32_t seen;   // a bit per key, 16: first unit of a pair (here), 17: last unit (here)
+  int n, tile;     // tile: bit 30: the pair's first unit here, bit 31: its last one here
+  uint32_t seen;   // a bit per key
   int left;        // units of the pair behind it
+  __device__ __forceinline__ int which() const { return tile & 0x3FFFFFFF; }
+  __device__ __forceinline__ bool first() const { return tile >> 30 & 1; }
+  __device__ __forceinline__ bool last() const { return tile < 0; }
 };
 
 template <typename Tile, typename C, int HD, int WARPS, int STAGES>
@@ -610,7 +624,7 @@ template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES, 
 __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn p, Parts parts) {
   using S = Shape<Tile, C, HD, WARPS, STAGES>;
   constexpr int ROWS = Tile::ROWS, RB = HD * (int)sizeof(C), kThreads = WARPS * 32, kKeys = Tile::kKeys;
-  constexpr uint32_t kAll = (1u << kKeys) - 1;
+  constexpr uint32_t kAll = kKeys == 32 ? 0xFFFFFFFFu : (1u << kKeys) - 1;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t sums[WARPS];
   __shared__ End ends_s[2];
@@ -697,7 +711,8 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
     for (int i = lane; i < STAGES * S::kStage / 16; i += 32) *(uint4*)(smem + warp * STAGES * S::kStage + i * 16) = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
-  const bool whole = a.page % kKeys == 0;   // a stage's keys lie on one page
+  constexpr int kRun = kKeys < 16 ? kKeys : 16;
+  const bool whole = a.page % kRun == 0;   // kRun neighbouring keys of a stage lie on one page
   const int row_key = lane & (kKeys - 1);
   // the filling side's key head
   const C *k_head, *v_head;
@@ -735,20 +750,25 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
       const uint32_t ks = ring + st * S::kStage;
       const int64_t page = held ? id : 0;
       if (whole && seen == kAll) {
-        // sixteen rows a fixed stride apart
-        const C* kr = k_head + page * a.kp_page + (off - row_key + r0) * a.kp_row + piece * (16 / (int)sizeof(C));
-        const C* vr = v_head + page * a.vp_page + (off - row_key + r0) * a.vp_row + piece * (16 / (int)sizeof(C));
+        // kRun rows of a page at a time, a fixed stride apart
 #pragma unroll
-        for (int i = 0; i < kKeys / RPI; ++i) {
-          const int row = i * RPI;   // swizzle(row + r0) = swizzle(row) ^ ((r0 & 1) << 2)
-          const uint32_t at = ks + row * RB + (lane_at ^ (Tile::swizzle(row) << 4));
+        for (int run = 0; run < kKeys; run += kRun) {
+          const int64_t pg = kKeys == kRun ? page : (int64_t)__shfl_sync(0xffffffffu, id, run);
+          const int row0 = kKeys == kRun ? off - row_key : __shfl_sync(0xffffffffu, off, run);
+          const C* kr = k_head + pg * a.kp_page + (row0 + r0) * a.kp_row + piece * (16 / (int)sizeof(C));
+          const C* vr = v_head + pg * a.vp_page + (row0 + r0) * a.vp_row + piece * (16 / (int)sizeof(C));
 #pragma unroll
-          for (int x = 0; x < CH; x += LPR) {
-            if (piece + x < k_pieces) cp16(at + x * 16, (const char*)kr + x * 16);
-            if (piece + x < v_pieces) cp16(at + kKeys * RB + x * 16, (const char*)vr + x * 16);
+          for (int i = 0; i < kRun / RPI; ++i) {
+            const int row = run + i * RPI;   // swizzle(row + r0) = swizzle(row) ^ ((r0 & 1) << 2)
+            const uint32_t at = ks + row * RB + (lane_at ^ (Tile::swizzle(row) << 4));
+#pragma unroll
+            for (int x = 0; x < CH; x += LPR) {
+              if (piece + x < k_pieces) cp16(at + x * 16, (const char*)kr + x * 16);
+              if (piece + x < v_pieces) cp16(at + kKeys * RB + x * 16, (const char*)vr + x * 16);
+            }
+            kr += RPI * a.kp_row;
+            vr += RPI * a.vp_row;
           }
-          kr += RPI * a.kp_row;
-          vr += RPI * a.vp_row;
         }
       } else {
         const int64_t ko = page * a.kp_page + off * a.kp_row, vo = page * a.vp_page + off * a.vp_row;
@@ -766,7 +786,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
           }
         }
       }
-      Meta me{n, tile, seen | (unit == 0 || filled == 0 ? 1u << 16 : 0), tok.units - 1 - unit};
+      Meta me{n, tile | (unit == 0 || filled == 0 ? 1 << 30 : 0), seen, tok.units - 1 - unit};
       ++filled;
       if (++unit == tok.units) {
         unit = 0;
@@ -782,7 +802,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
       }
       more = !ended();
       if (more) look();
-      if (me.left == 0 || !more) me.seen |= 1u << 17;
+      if (me.left == 0 || !more) me.tile |= 1 << 31;
       if (lane == 0) meta[warp][st] = me;
     }
     cp_commit();
@@ -795,7 +815,7 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
   Tile t;
   int slot = 0;   // 0: the pair at hand is the one that the stretch begins in, 1: a later one
   auto fetch = [&](const Meta& me) {
-    const int h = me.tile / tiles, g0 = (me.tile % tiles) * ROWS;
+    const int h = me.which() / tiles, g0 = (me.which() % tiles) * ROWS;
     if constexpr (Tile::kAhead) t.fetch(p, me.n, h * G + g0, min(ROWS, G - g0), lane);
   };
   __syncwarp();
@@ -807,20 +827,20 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
     __syncwarp();
     const int st = s % STAGES;
     const Meta me = meta[warp][st];
-    const int h = me.tile / tiles, g0 = (me.tile % tiles) * ROWS, rows = min(ROWS, G - g0);
-    if (me.seen >> 16 & 1) {
+    const int h = me.which() / tiles, g0 = (me.which() % tiles) * ROWS, rows = min(ROWS, G - g0);
+    if (me.first()) {
       slot = s > 0;
       t.reset(p, me.n, h * G + g0, rows, p.scale_log2e * (a.k_scale ? a.k_scale[h] : 1.f), lane, scratch);
     }
-    if (s + 1 < filled && (meta[warp][(s + 1) % STAGES].seen >> 16 & 1)) fetch(meta[warp][(s + 1) % STAGES]);
+    if (s + 1 < filled && meta[warp][(s + 1) % STAGES].first()) fetch(meta[warp][(s + 1) % STAGES]);
     const uint32_t ks = ring + st * S::kStage;
-    if (me.seen & kAll) t.step(p, ks, ks + kKeys * RB, me.seen & kAll, lane, scratch);
-    if (!(me.seen >> 17 & 1)) continue;
+    if (me.seen) t.step(p, ks, ks + kKeys * RB, me.seen, lane, scratch);
+    if (!me.last()) continue;
 
     // the pair's end in this CTA: join the warps, and finish the pair or leave a partial
     const bool begins = slot || first_unit == 0, complete = begins && me.left == 0;
     if (begins && !complete && tid == 0)   // the pair's end on the line, and the CTA whose stretch holds it
-      parts.cuts[blockIdx.x] = Cut{me.n, me.tile, (int)(((hi + me.left) * ctas - 1) / total), slot};
+      parts.cuts[blockIdx.x] = Cut{me.n, me.which(), (int)(((hi + me.left) * ctas - 1) / total), slot};
     t.finish(ml_s[warp], lane);
     const float vscale = a.v_scale ? a.v_scale[h] : 1.f;
     const int64_t part0 = ((int64_t)blockIdx.x * 2 + slot) * ROWS;
@@ -984,10 +1004,10 @@ template <typename T, int ROWS>
 cudaError_t launch_mma(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int w = p.a.E > p.a.D ? p.a.E : p.a.D;
   if (p.a.cache_dtype == THIN_ATTN_E4M3) {
-    if (w <= 128) return launch_tile<MmaTile<T, e4m3, 128, ROWS>, T, e4m3, 128, 4, 3, 3>(p, ws, st);
+    if (w <= 128) return launch_tile<MmaTile<T, e4m3, 128, ROWS>, T, e4m3, 128, 4, 3, 2>(p, ws, st);
     return launch_tile<MmaTile<T, e4m3, 256, ROWS>, T, e4m3, 256, 4, 3, 2>(p, ws, st);
   }
-  if (w <= 64) return launch_tile<MmaTile<T, T, 64, ROWS>, T, T, 64, 4, ROWS == 8 ? 4 : 3, 3>(p, ws, st);
+  if (w <= 64) return launch_tile<MmaTile<T, T, 64, ROWS>, T, T, 64, 4, 3, 2>(p, ws, st);
   if (w <= 128) return launch_tile<MmaTile<T, T, 128, ROWS>, T, T, 128, 4, 3, 2>(p, ws, st);
   return launch_tile<MmaTile<T, T, 256, ROWS>, T, T, 256, 4, 3, 1>(p, ws, st);
 }
