@@ -563,3 +563,128 @@ def test_refusals_on_the_device():
                 lambda: T.paged_plan(i32([0] * 16385), i32([0] * 16385), i32([[0]] * 16385), i32([0]), i32([1]), 16, 4)):
         with pytest.raises(T.ThinAttnError, match="EINVAL|EUNSUPPORTED"):
             bad()
+
+
+@pytest.mark.parametrize("dtype,cache,G", [("fp16", "fp16", 4), ("fp16", "fp16", 12), ("bf16", "e4m3", 4), ("bf16", "bf16", 4), ("fp32", "fp32", 4)])
+def test_a_long_tail_of_small_weights(dtype, cache, G):
+    """One key with weight near 1 and 60000 others at 2^-25 of it: together 0.2% of the sum, which a 16-bit weight
+    rounds up or away unless it is scaled."""
+    L, E, page = 60001, 64, 64
+    kp, vp, (ks, vs), table, _ = filled([L], 1, E, E, page, dtype, cache, 21)
+    q = torch.zeros(1, G, E, dtype=TYPES[dtype], device=DEV)
+    q[..., 0] = 1.0
+    ids = table[0, :-(-L // page)].long()
+    K, V = torch.zeros(L, E, dtype=torch.float64), torch.ones(L, E, dtype=torch.float64)
+    K[0, 0], V[0] = 16.0, 0.0
+    if cache == "e4m3":
+        ks.fill_(1.0)
+        vs.fill_(1.0)
+    k, v = torch.zeros(len(ids) * page, E), torch.zeros(len(ids) * page, E)
+    k[:L], v[:L] = K.float(), V.float()
+    kp[ids] = k.view(len(ids), 1, page, E).to(DEV).to(kp.dtype)
+    vp[ids] = v.view(len(ids), 1, page, E).to(DEV).to(vp.dtype)
+    scale = 25.4 * math.log(2) / 16.0
+    out, lse = T.paged_attention(q, kp, vp, table, i32([L]), scale=scale, k_scale=ks, v_scale=vs, return_lse=True)
+    check(out[0], lse[0], q[0], [(K.to(DEV), V.to(DEV))], dtype, cache, scale)
+
+
+def test_output_in_place_of_the_queries():
+    kp, vp, _, table, held = filled([300, 1, 4097], 2, 64, 64, 16, "bf16", "bf16", 22)
+    q = rnd(torch.Generator(DEV).manual_seed(23), 3, 8, 64).bfloat16()
+    want = T.paged_attention(q, kp, vp, table, i32([300, 1, 4097]))
+    T.paged_attention(q, kp, vp, table, i32([300, 1, 4097]), out=q)
+    assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("page,tokens", [(2048, 5000), (65536, 3000), (100, 777)])
+def test_append_of_long_runs(page, tokens):
+    """Runs that span many blocks of tokens, beginning within a page and at its start."""
+    gen = torch.Generator(DEV).manual_seed(page)
+    kp, vp, _ = pool(gen, 4, 3, page, 16, 16, "bf16")
+    b = (torch.zeros(4, 3, 2, 16, dtype=torch.int8, device=DEV), torch.zeros(4, 3, dtype=torch.int8, device=DEV))
+    table, L = [2, 0, 3, 1], 0
+    for n in (37, tokens if page > 1000 else 300):
+        n = min(n, 4 * page - L)
+        at = torch.arange(L, L + n, device=DEV)
+        slots = i32(table).long()[at // page] * page + at % page
+        k, v = rnd(gen, n, 3, 16).bfloat16(), rnd(gen, n, 3, 16).bfloat16()
+        T.paged_append(k, v, slots, kp, vp, bounds=b)
+        assert torch.equal(kp[slots // page, :, slots % page], k) and torch.equal(vp[slots // page, :, slots % page], v)
+        L += n
+    bw, xw = bounds_of(kp, i32([table]), [L], page)
+    used = i32(table[:-(-L // page)]).long()
+    assert torch.equal(b[0][used], bw[used]) and torch.equal(b[1][used], xw[used])
+
+
+def test_an_8_bit_cache_through_its_class():
+    gen = torch.Generator(DEV).manual_seed(31)
+    H, G, E, D, R = 2, 4, 64, 32, 3
+    ks, vs = torch.full((H,), 0.02, device=DEV), torch.full((H,), 0.03, device=DEV)
+    cache = T.PagedAttentionCache(20, 16, H, E, D, torch.float16, R, 100, cache_dtype=torch.float8_e4m3fn, bounds=True, k_scale=ks,
+                                  v_scale=vs, scale=0.2)
+    p = cache.plan(i32([30, 0, 17]), 50)
+    k, v = rnd(gen, 50, H, E).half(), rnd(gen, 50, H, D).half()
+    cache.append(k, v, p.slots)
+    q = rnd(gen, R, H * G, E).half()
+    out, lse = cache.attend(q, return_lse=True)
+    both, lse2, pages = cache.attend_sparse(q, 8, return_lse=True, return_pages=True)
+    held = lambda x, s: (x.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).double() * s.double()[:, None]
+    for r, (a, b) in enumerate([(0, 30), (30, 30), (30, 47)]):
+        K, V = held(k[a:b], ks), held(v[a:b], vs)
+        for o, l in ((out, lse), (both, lse2)):
+            check(o[r], l[r], q[r], [(K[:, h], V[:, h]) for h in range(H)], "fp16", "e4m3", 0.2)
+    assert pages[0].tolist() == [[0, 1] + [-1] * 6] * H and pages[1].tolist() == [[-1] * 8] * H
+    with pytest.raises(ValueError):
+        T.PagedAttentionCache(20, 16, H, E, D, torch.float16, R, 100, cache_dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="bounds"):
+        T.PagedAttentionCache(20, 16, H, E, D, torch.float16, R, 100).attend_sparse(q, 4)
+
+
+def test_calls_from_two_threads_and_streams():
+    """Concurrent calls that share only inputs: each gets the result that it gets alone."""
+    import threading
+    lengths = [700, 0, 64, 5000]
+    kp, vp, _, table, _ = filled(lengths, 2, 64, 64, 16, "bf16", "bf16", 41)
+    b = bounds_of(kp, table, lengths, 16)
+    qs = [rnd(torch.Generator(DEV).manual_seed(50 + i), 4, 8, 64).bfloat16() for i in range(4)]
+    n = i32(lengths)
+    want = [(T.paged_attention(q, kp, vp, table, n), T.paged_sparse_attention(q, kp, vp, table, n, b, 6)) for q in qs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [(T.paged_attention(qs[i], kp, vp, table, n), T.paged_sparse_attention(qs[i], kp, vp, table, n, b, 6)) for _ in range(30)]
+            torch.cuda.current_stream().synchronize()
+        wrong.extend(1 for g in got if not (torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1])))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_first_use_inside_a_capture():
+    """A process whose first call of every operator is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch, thinned_softmax_attention_b200 as T
+c = T.PagedAttentionCache(20, 16, 2, 64, 64, torch.bfloat16, 3, 100, bounds=True)
+new = torch.tensor([5, 20, 1], dtype=torch.int32, device="cuda")
+k = torch.randn(26, 2, 64, device="cuda").bfloat16(); q = torch.randn(3, 8, 64, device="cuda").bfloat16()
+keep = torch.tensor([-1, 4, 0], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    p = c.plan(new, 26); c.append(k, k, p.slots); a = c.attend(q); b = c.attend_sparse(q, 8); c.release(keep)
+assert c.lengths.tolist() == [0, 0, 0]
+g.replay(); torch.cuda.synchronize()
+assert c.lengths.tolist() == [5, 4, 0], c.lengths
+assert torch.isfinite(a).all() and (a - b).abs().max() < 1e-1 and a.abs().max() > 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert "captured" in r.stdout, r.stdout + r.stderr

@@ -314,27 +314,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) append_kerne
   }
   if (!a.bounds) return;
 
-  // tokens behind the block that go on with its last run, and whether one of them is its page's first slot
-  int tail = 0;
-  bool tail_anew = false;
-  if (page_s[block] >= 0) {
-    const int64_t begin = (int64_t)page_s[block] * a.page;
-    for (;;) {
-      const uint32_t in = __ballot_sync(0xffffffffu, behind >= begin && behind < begin + a.page);
-      const int run = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-      tail_anew |= __any_sync(0xffffffffu, lane < run && behind == begin);
-      tail += run;
-      if (run < 32) break;
-      const int t = t0 + block + tail + lane;
-      behind = t < a.N ? a.slots[t] : -1;
-    }
-  }
-  // of the runs that begin in a block all but the last end in it: at most four of 64 tokens have more than
-  // kShort, two of 32 (keys wider than 128: kPieces turns), one of kFew
-  constexpr int kLongs = 64;   // runs times threads of a row
-  __shared__ __align__(16) Lane8<C> part[kLongs * 2 * kWarps];
-  const int per = 1 << k_shift, col = (lane & (per - 1)) * 8, sub = lane >> k_shift, rows = 32 >> k_shift;
-  int shorts = 0, longs = 0;
   // bit i: token i begins a run, or goes to its page's first slot
   uint64_t starts = 0, fresh = 0;
 #pragma unroll
@@ -343,6 +322,37 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) append_kerne
     starts |= (uint64_t)__ballot_sync(0xffffffffu, i < block && (i == 0 || page_s[i + 1] != page_s[i])) << x2;
     fresh |= (uint64_t)__ballot_sync(0xffffffffu, i < block && page_s[i + 1] >= 0 && off_s[i] == 0) << x2;
   }
+  // tokens behind the block that go on with a run that begins in it, and whether one of them is its
+  // page's first slot: 32 at first, then kScan * 32 at a time
+  int tail = 0;
+  bool tail_anew = false;
+  if (page_s[block] >= 0 && (starts > 1 || page_s[1] != page_s[0])) {
+    const int64_t begin = (int64_t)page_s[block] * a.page;
+    constexpr int kScan = 8;
+    auto scan = [&](int64_t slot) {   // whether the run goes on behind these 32
+      const uint32_t in = __ballot_sync(0xffffffffu, slot >= begin && slot < begin + a.page);
+      const int run = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+      tail_anew |= __any_sync(0xffffffffu, lane < run && slot == begin);
+      tail += run;
+      return run == 32;
+    };
+    bool on = scan(behind);
+    while (on) {
+      int64_t slot[kScan];
+      const int from = t0 + block + tail + lane;
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) slot[u] = from + 32 * u < a.N ? a.slots[from + 32 * u] : -1;
+#pragma unroll
+      for (int u = 0; u < kScan; ++u)
+        if (on) on = scan(slot[u]);
+    }
+  }
+  // of the runs that begin in a block all but the last end in it: at most four of 64 tokens have more than
+  // kShort, two of 32 (keys wider than 128: kPieces turns), one of kFew
+  constexpr int kLongs = 64;   // runs times threads of a row
+  __shared__ __align__(16) Lane8<C> part[kLongs * 2 * kWarps];
+  const int per = 1 << k_shift, col = (lane & (per - 1)) * 8, sub = lane >> k_shift, rows = 32 >> k_shift;
+  int shorts = 0, longs = 0;
   // every run that begins in the block: its first token, its tokens, its page, whether it starts the page anew
   auto runs = [&](auto&& f) {
     for (uint64_t left = starts; left;) {

@@ -138,6 +138,9 @@ struct MmaTile {
   static constexpr bool kSplit = !k8 || ROWS == 8;            // P as two numbers
   static constexpr int kKeys = RB <= 128 ? 32 : 16;           // keys of a stage: short rows, twice as many for the same overhead
   static constexpr int NB = kKeys / 16;                       // products' blocks of 16 keys
+  // fp16 weights are lifted by 2^14: without that those below 2^-14 of the largest lose bits, and a long
+  // tail of keys at 2^-25 is rounded up or away as a whole
+  static constexpr float kLift = std::is_same<M, __half>::value ? 16384.f : 1.f;
   static_assert(ROWS == 8 || ROWS == 16, "");
   static_assert(VI >= 1 && KJ == 2 * VI, "");
 
@@ -291,10 +294,11 @@ struct MmaTile {
         for (int t = 0; t < 2; ++t) {
           const float p0 = ex2(s[b][t][2 * x] - ref), p1 = ex2(s[b][t][2 * x + 1] - ref);
           sum += p0 + p1;
-          hi[x][b][t] = pack2<M>(p0, p1);
+          const float w0 = p0 * kLift, w1 = p1 * kLift;
+          hi[x][b][t] = pack2<M>(w0, w1);
           if constexpr (kSplit) {
             const float2 h = unpack2<M>(hi[x][b][t]);
-            lo[x][b][t] = pack2<M>(p0 - h.x, p1 - h.y);
+            lo[x][b][t] = pack2<M>(w0 - h.x, w1 - h.y);
           }
         }
       l[x] = l[x] * f[x] + sum;
@@ -385,12 +389,14 @@ struct MmaTile {
 #pragma unroll
         for (int y = 0; y < DC; y += 4) {
           const int col = (d % COLS + y) / 4;
+          constexpr float by = 1.f / kLift;
           if constexpr (ROWS == 8) {
-            dst[place(r, col)] = make_float4(o[i][y][u] + o[i][y][2 + u], o[i][y + 1][u] + o[i][y + 1][2 + u],
-                                             o[i][y + 2][u] + o[i][y + 2][2 + u], o[i][y + 3][u] + o[i][y + 3][2 + u]);
+            dst[place(r, col)] = make_float4((o[i][y][u] + o[i][y][2 + u]) * by, (o[i][y + 1][u] + o[i][y + 1][2 + u]) * by,
+                                             (o[i][y + 2][u] + o[i][y + 2][2 + u]) * by, (o[i][y + 3][u] + o[i][y + 3][2 + u]) * by);
           } else {
-            dst[place(r, col)] = make_float4(o[i][y][u], o[i][y + 1][u], o[i][y + 2][u], o[i][y + 3][u]);
-            dst[place(r + 8, col)] = make_float4(o[i][y][2 + u], o[i][y + 1][2 + u], o[i][y + 2][2 + u], o[i][y + 3][2 + u]);
+            dst[place(r, col)] = make_float4(o[i][y][u] * by, o[i][y + 1][u] * by, o[i][y + 2][u] * by, o[i][y + 3][u] * by);
+            dst[place(r + 8, col)] =
+                make_float4(o[i][y][2 + u] * by, o[i][y + 1][2 + u] * by, o[i][y + 2][2 + u] * by, o[i][y + 3][2 + u] * by);
           }
         }
       }
