@@ -1,15 +1,18 @@
-"""Build libthin_attn.so in-tree for sm_100a with nvcc.
+"""Build libthin_attn.so in-tree for sm_100a with nvcc, and the paged operators' Python binding with g++.
 
     python -m thinned_softmax_attention_b200.build [--force]
 """
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libthin_attn.so")
+BINDING = os.path.join(HERE, "_paged.so")
+BINDING_SOURCE = os.path.join(HERE, "csrc", "paged_binding.cpp")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
 
@@ -23,15 +26,41 @@ def headers():
                   + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
+def newer(target, inputs):
+    """Whether the target exists and none of its inputs has changed since."""
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in inputs + [__file__])
+
+
 def up_to_date():
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in sources() + headers() + [__file__])
+    return newer(LIB, sources() + headers()) and newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "thin_attn.h")])
+
+
+def build_binding():
+    """_paged.so against the installed torch (its C++ ABI and libraries)."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(os.environ.get("NVCC", "nvcc"))))), "include")
+    tmp = BINDING + ".tmp"
+    # nvcc's host compiler, whose C++ library is torch's too (a compiler that links its own statically is not)
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                           "-isystem", os.path.join(base, "include"),
+                           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-I", os.path.join(ROOT, "include"),
+                           BINDING_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                           "-ltorch", "-ltorch_python"])
+    os.replace(tmp, BINDING)
 
 
 def build(force=False, verbose=False):
     if not force and up_to_date():
+        return LIB
+    if force or not newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "thin_attn.h")]):
+        build_binding()
+    if not force and newer(LIB, sources() + headers()):
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     objdir = os.path.join(ROOT, "_build")
