@@ -215,8 +215,21 @@ struct Stored {
   int exp;
 };
 
-// A warp writes the bounds of one page and head: of `g` alone, or the stored ones widened.  Lanes of the same
-// channels hold the same range.
+// Whole numbers and floats by the exponent of 2^23: no conversions, which run at a quarter of the rate or less.
+// floor and ceil of |x| <= 127 as the low byte of the result.
+__device__ __forceinline__ uint32_t floor_byte(float x) { return __float_as_uint(__fadd_rd(x, 12582912.f)); }
+__device__ __forceinline__ uint32_t ceil_byte(float x) { return __float_as_uint(__fadd_ru(x, 12582912.f)); }
+// Byte i of w, a signed one with its top bit inverted.
+__device__ __forceinline__ float signed_byte(uint32_t w, int i) {
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | i)) - 8388736.f;
+}
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// A warp writes the bounds of one page and head: of `g` alone, or the stored ones widened, which is the same as
+// the bounds of both's values: floor(floor(u) / 2^s) = floor(u / 2^s).  Lanes of the same channels hold
+// the same range.
 template <typename C>
 __device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& a, const Range<C>& g, const Stored& old, bool anew,
                                              int64_t at, int col, bool writes, int lane) {
@@ -229,27 +242,29 @@ __device__ __forceinline__ void write_bounds(const thin_attn_paged_append_args& 
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int x1 = bound_exponent(m), x = anew ? x1 : max(x1, old.exp);
-  const int up = min(anew ? 0 : x - old.exp, 31);   // the stored bounds' steps grow by 2^up
+  int x = bound_exponent(m);
+  if (!anew) {
+    x = max(x, min(max(old.exp, kBoundMin), kBoundMax));
+    const float step = pow2f(min(max(old.exp, kBoundMin), kBoundMax));
+    const uint32_t l[2] = {old.lo.x ^ 0x80808080u, old.lo.y ^ 0x80808080u}, h[2] = {old.hi.x ^ 0x80808080u, old.hi.y ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = fminf(lo[i], signed_byte(l[i >> 2], i & 3) * step);
+      hi[i] = fmaxf(hi[i], signed_byte(h[i >> 2], i & 3) * step);
+    }
+  }
   if (lane == 0) a.exps[at] = (int8_t)x;
   if (!writes || col >= a.E) return;
   const float inv = pow2f(-x);
-  uint32_t wl[2] = {0, 0}, wh[2] = {0, 0};
+  uint32_t l[8], h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int l = (int)fminf(fmaxf(floorf(lo[i] * inv), -127.f), 127.f);
-    int u = (int)fminf(fmaxf(ceilf(hi[i] * inv), -127.f), 127.f);
-    if (!anew) {
-      const int sl = (int8_t)((i < 4 ? old.lo.x : old.lo.y) >> (8 * (i & 3))), sh = (int8_t)((i < 4 ? old.hi.x : old.hi.y) >> (8 * (i & 3)));
-      l = min(l, sl >> up);
-      u = max(u, -((-sh) >> up));
-    }
-    wl[i >> 2] |= (uint32_t)(l & 0xFF) << (8 * (i & 3));
-    wh[i >> 2] |= (uint32_t)(u & 0xFF) << (8 * (i & 3));
+    l[i] = floor_byte(fminf(fmaxf(lo[i] * inv, -127.f), 127.f));
+    h[i] = ceil_byte(fminf(fmaxf(hi[i] * inv, -127.f), 127.f));
   }
   int8_t* row = a.bounds + at * 2 * a.E;
-  *(uint2*)(row + col) = make_uint2(wl[0], wl[1]);
-  *(uint2*)(row + a.E + col) = make_uint2(wh[0], wh[1]);
+  *(uint2*)(row + col) = make_uint2(low_bytes(l[0], l[1], l[2], l[3]), low_bytes(l[4], l[5], l[6], l[7]));
+  *(uint2*)(row + a.E + col) = make_uint2(low_bytes(h[0], h[1], h[2], h[3]), low_bytes(h[4], h[5], h[6], h[7]));
 }
 
 template <typename T, typename C>
