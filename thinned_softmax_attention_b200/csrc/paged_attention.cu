@@ -27,6 +27,18 @@
 //
 // fp32 caches use the tf32 products (m16n8k8) with every operand as the sum of two tf32 numbers,
 // (a_hi + a_lo)(b_hi + b_lo), good to 2^-22.  The upper rows of the tile carry a_lo, so that takes two products.
+//
+// These are the 16-row products on purpose: tcgen05 tiles have 64 or 128 rows, of which G would fill a few,
+// and their operands pass through shared memory in fixed layouts, P included.  The tensor pipe is no bound here
+// (24% busy at e4m3, the densest case).
+//
+// B200 (copy rate 6.46 TB/s), width 128, bf16, 4 query rows to a key head unless stated:
+//   16 requests of 65536 .. 131072 keys, 8 heads     0.91 .. 0.95 ms   6.9 .. 6.6 TB/s
+//   48 requests of 1 .. 8192 keys, 8 heads           54 us             5.5 TB/s     16 query rows: 63 us
+//   20 requests of 32768 keys, 8 heads, e4m3         0.22 ms           6.0 TB/s
+//   16 requests of up to 65536 keys, fp32            1.7 ms            5.0 TB/s
+//   1 request of 500 keys, 32 heads                  9.8 us            (6.4 of them with 64 keys)
+// What is left is the 10 us at the ends: launch, lengths, first reads, join.
 #include <type_traits>
 
 #include "paged.h"
@@ -623,7 +635,8 @@ struct End {
 
 // A pair's stretch of the line: its units, and kPairCost more before them for what a pair costs besides
 // its keys (the join of the warps, the outputs), in units.  Without them a stretch full of short
-// requests takes several times as long as one within a long request.
+// requests takes several times as long as one within a long request (the 48 requests above: 0 units 101 us, 1 to
+// 4 units 55 to 56; width 256: 1 unit 159, 2 units 122; width 64: 2 units 41, 4 units 43).
 constexpr int kPairCost = 2;
 
 template <typename Tile, typename T, typename C, int HD, int WARPS, int STAGES, int PER_SM>
@@ -971,6 +984,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(PagedAttn p, Part
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Query rows of a tile: up to 8 leave its upper half for the operands' lower parts, 9 to 16 fill it (fp32 has
+// only the first form); more are several tiles, whose keys come from L2 for all but one.
 int rows_of(const thin_attn_paged_attention_args& a) {
   return a.dtype == THIN_ATTN_FP32 || a.Hq / a.H <= 8 ? 8 : 16;
 }
@@ -1021,6 +1036,9 @@ cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, parts, (int)Tile::ROWS);
 }
 
+// By the wider of E and D, rounded up to the stage's row; narrower rows are padded in shared memory, not in
+// the reads.  Warps, stages and CTAs per SM fill the 227 KB with 64 KB and more of reads in flight per SM.  Rows of up to
+// 128 bytes come 32 keys to a stage (16 keys: the e4m3 requests above 0.26 ms).
 template <typename T, int ROWS>
 cudaError_t launch_mma(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int w = p.a.E > p.a.D ? p.a.E : p.a.D;

@@ -9,14 +9,18 @@
 // dependent latencies (lengths, sums, search, page id), so one CTA takes it all while the tokens are few,
 // and a second launch spreads the tokens over the GPU when they are many.  Both sums are taken at
 // once, as if every token had room; only where one has not are the pages summed again.
+// B200: 64 requests of one token 3.5 us, 512 of them 5.4, 65536 tokens of 512 requests 13 us.
 #include "paged.h"
 
 namespace thin {
 
 namespace {
 
-constexpr int kThreads = 1024, kFewThreads = 256;   // of the first launch
-constexpr int kFillHere = 2048;                     // tokens that it places itself
+// Of the first launch; 64 requests with 256 threads 3.6 us, with 1024 4.6.
+constexpr int kThreads = 1024, kFewThreads = 256;
+// Tokens that the first launch places itself: alone and with the second launch 3.6 and 5.8 us for 64 tokens,
+// 7.0 and 7.2 for 4096, 8.5 and 7.7 for 8192, 67 and 13 for 65536.
+constexpr int kFillHere = 4096;
 constexpr int kFillThreads = 256;
 constexpr int kOwnPages = 2;                        // fresh pages that a request's thread enters itself
 

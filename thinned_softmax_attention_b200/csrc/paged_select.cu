@@ -15,6 +15,9 @@
 // taken by a radix search, 10 bits a round from the leading bit of (largest - smallest word); it ends as
 // soon as a bin is taken whole, mostly in the second round.  Then it writes the pages above that
 // word, and the first of those on it, in ascending order.
+// Latency bounds both (a scoring CTA's chain: length, page id, bounds).  B200: 32 requests of up to 2048 pages,
+// 8 heads: scoring 18 us (34 MB of bounds), choice 10; one request of 1024 pages 8 and 9.  One launch with a
+// cluster per (token, head) took 37 us for the batch: its meetings cost more than the second launch.
 #include "paged.h"
 #include "paged_types.cuh"
 
@@ -325,6 +328,7 @@ template <typename T, int KJ>
 cudaError_t score_t(const thin_attn_paged_attention_args& a, uint32_t* words, cudaStream_t st) {
   const int rows = (a.Hq / a.H + 15) & ~15;
   // 128 pages per CTA, one turn, while those CTAs run at once (four per SM); four turns where there are more
+  // (the batch above with its attention: 80 us at 128 pages, 77 at 512, 83 at 1024)
   int per = 128;
   if ((int64_t)((a.W + per - 1) / per) * a.N * a.H > 148 * 4) per = 512;
   const size_t smem = (size_t)rows * q_stride(a.E) + rows * 4;
