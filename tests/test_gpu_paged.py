@@ -688,3 +688,20 @@ print("captured")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert "captured" in r.stdout, r.stdout + r.stderr
+
+
+def test_lengths_close_to_31_bits():
+    """A table that names one page 42949 times: 2147450000 keys, whose count plus a page passes 31 bits."""
+    gen = torch.Generator(DEV).manual_seed(32)
+    page, W, E = 50000, 42949, 64
+    kp, vp = (rnd(gen, 1, 1, page, E).bfloat16() for _ in range(2))
+    b = (torch.zeros(1, 1, 2, E, dtype=torch.int8, device=DEV), torch.zeros(1, 1, dtype=torch.int8, device=DEV))
+    q, table = rnd(gen, 1, 4, E).bfloat16(), torch.zeros(1, W, dtype=torch.int32, device=DEV)
+    K, V = kp[0, 0].double(), vp[0, 0].double()
+    for last in (page, 49000):
+        length = i32([(W - 1) * page + last])
+        out, lse, pages = T.paged_sparse_attention(q, kp, vp, table, length, b, 4, return_lse=True, return_pages=True)
+        assert pages.tolist() == [[[0, 1, 2, W - 1]]]
+        check(out[0], lse[0], q[0], [(torch.cat((K, K, K, K[:last])), torch.cat((V, V, V, V[:last])))], "bf16", "bf16")
+        out, lse = T.paged_attention(q, kp, vp, table, length, window=70, return_lse=True)
+        check(out[0], lse[0], q[0], [(K[last - 70:last], V[last - 70:last])], "bf16", "bf16")

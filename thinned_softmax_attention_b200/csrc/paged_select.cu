@@ -36,7 +36,7 @@ __device__ __forceinline__ bool token_pages(const thin_attn_paged_attention_args
   *row = a.rows ? a.rows[n] : n;
   if (*row < 0 || *row >= a.R) return false;
   *len = min(max(a.lengths[n], 0), a.W * a.page);
-  *pages = (*len + a.page - 1) / a.page;
+  *pages = (int)(((uint32_t)*len + a.page - 1) / (uint32_t)a.page);   // the sum may pass 31 bits
   return true;
 }
 
