@@ -705,3 +705,17 @@ def test_lengths_close_to_31_bits():
         check(out[0], lse[0], q[0], [(torch.cat((K, K, K, K[:last])), torch.cat((V, V, V, V[:last])))], "bf16", "bf16")
         out, lse = T.paged_attention(q, kp, vp, table, length, window=70, return_lse=True)
         check(out[0], lse[0], q[0], [(K[last - 70:last], V[last - 70:last])], "bf16", "bf16")
+
+
+def test_strides_of_axes_of_one_are_free():
+    """One token, one key head, one page: what their axes' strides say is never used."""
+    gen = torch.Generator(DEV).manual_seed(31)
+    E, L = 64, 16
+    new = [rnd(gen, L, 1, E).bfloat16().as_strided((L, 1, E), (E, 3, 1)) for _ in range(2)]
+    kp, vp = (torch.zeros(L * E, dtype=torch.bfloat16, device=DEV).as_strided((1, 1, L, E), (5, 7, E, 1)) for _ in range(2))
+    T.paged_append(*new, torch.arange(L, device=DEV), kp, vp)
+    assert torch.equal(kp[0, 0], new[0][:, 0]) and torch.equal(vp[0, 0], new[1][:, 0])
+    q = rnd(gen, 4, E).bfloat16().as_strided((1, 4, E), (9, E, 1))
+    out, lse = torch.empty(4 * E, dtype=torch.bfloat16, device=DEV).as_strided((1, 4, E), (11, E, 1)), torch.empty(1, 4, device=DEV)
+    T.paged_attention(q, kp, vp, i32([[0]]), i32([L]), out=out, lse=lse)
+    check(out[0], lse[0], q[0], [(kp[0, 0].double(), vp[0, 0].double())], "bf16", "bf16")

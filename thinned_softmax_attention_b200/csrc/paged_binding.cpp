@@ -71,6 +71,9 @@ bool flag(PyObject* o) {
   return v != 0;
 }
 
+// A stride that is used: that of an axis of one may be any number.
+int64_t stride_of(const at::Tensor& t, int axis) { return t.size(axis) > 1 ? t.stride(axis) : 0; }
+
 std::string place(const at::Tensor& t) {
   std::string s = std::string(c10::toString(t.scalar_type())) + " (";
   for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
@@ -312,19 +315,19 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.page = pool.page;
     p.n_pages = pool.n_pages;
     p.k = k.data_ptr();
-    p.k_token = k.stride(0);
-    p.k_head = k.stride(1);
+    p.k_token = stride_of(k, 0);
+    p.k_head = stride_of(k, 1);
     p.v = v.data_ptr();
-    p.v_token = v.stride(0);
-    p.v_head = v.stride(1);
+    p.v_token = stride_of(v, 0);
+    p.v_head = stride_of(v, 1);
     p.k_pages = kp.data_ptr();
-    p.kp_page = kp.stride(0);
-    p.kp_head = kp.stride(1);
-    p.kp_row = kp.stride(2);
+    p.kp_page = stride_of(kp, 0);
+    p.kp_head = stride_of(kp, 1);
+    p.kp_row = stride_of(kp, 2);
     p.v_pages = vp.data_ptr();
-    p.vp_page = vp.stride(0);
-    p.vp_head = vp.stride(1);
-    p.vp_row = vp.stride(2);
+    p.vp_page = stride_of(vp, 0);
+    p.vp_head = stride_of(vp, 1);
+    p.vp_row = stride_of(vp, 2);
     p.k_scale = s.k;
     p.v_scale = s.v;
     p.bounds = b.lohi;
@@ -381,16 +384,16 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.first = int32_of(a[13], "first");
     p.last = int32_of(a[14], "last");
     p.q = q.data_ptr();
-    p.q_token = q.stride(0);
-    p.q_head = q.stride(1);
+    p.q_token = stride_of(q, 0);
+    p.q_head = stride_of(q, 1);
     p.k_pages = kp.data_ptr();
-    p.kp_page = kp.stride(0);
-    p.kp_head = kp.stride(1);
-    p.kp_row = kp.stride(2);
+    p.kp_page = stride_of(kp, 0);
+    p.kp_head = stride_of(kp, 1);
+    p.kp_row = stride_of(kp, 2);
     p.v_pages = vp.data_ptr();
-    p.vp_page = vp.stride(0);
-    p.vp_head = vp.stride(1);
-    p.vp_row = vp.stride(2);
+    p.vp_page = stride_of(vp, 0);
+    p.vp_head = stride_of(vp, 1);
+    p.vp_row = stride_of(vp, 2);
     size_t bytes = 0;
     thin_attn_status status = fns.workspace(&p, &bytes);   // the shapes' refusals, before anything is allocated
     if (status != THIN_ATTN_OK) return PyLong_FromLong(status);
@@ -424,8 +427,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.workspace = ws.data_ptr();
     p.workspace_bytes = bytes;
     p.out = out.data_ptr();
-    p.out_token = out.stride(0);
-    p.out_head = out.stride(1);
+    p.out_token = stride_of(out, 0);
+    p.out_head = stride_of(out, 1);
     p.lse = lse.defined() ? (float*)lse.data_ptr() : nullptr;
     status = launch(fns.attention, p, dev);
     if (status != THIN_ATTN_OK) return PyLong_FromLong(status);
