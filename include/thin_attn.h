@@ -356,7 +356,8 @@ THIN_ATTN_API thin_attn_status thin_attn_halve_noalloc(int dtype, const void* K,
  * request r with cu[r] <= t < cu[r + 1], cu the prefix sums of max(n_new, 0):
  *   slots[t], rows[t] = r, context[t] = the tokens of r up to and with t (t's position + 1)
  * and -1, -1, 0 for tokens of requests that were not placed and for t >= cu[R].
- * lengths_out and n_free_out may be lengths and n_free themselves.  At most 16384 requests. */
+ * lengths_out and n_free_out may be lengths and n_free themselves.  At most 16384 requests; rows of the
+ * table may not overlap. */
 typedef struct {
   uint32_t struct_size;
   int32_t device, R, W, page, n_pages, max_tokens, reserved;   /* n_pages: entries of free_pages */
@@ -377,7 +378,9 @@ typedef struct {
 THIN_ATTN_API thin_attn_status thin_attn_paged_plan(const thin_attn_paged_plan_args* a, void* stream);
 
 /* Shorten request r to keep[r] tokens (0: it has ended; negative or beyond its length: as it is) and
- * push the pages behind them on the free stack, in order of requests; their table entries become -1. */
+ * push the pages behind them on the free stack, in order of requests, as the table holds them; their
+ * table entries become -1.  A page that two requests share comes back twice.  A page keeps its bounds, which
+ * later keys widen until one goes to its first slot. */
 typedef struct {
   uint32_t struct_size;
   int32_t device, R, W, page, n_pages;
@@ -397,9 +400,9 @@ THIN_ATTN_API thin_attn_status thin_attn_paged_release(const thin_attn_paged_rel
  * k that the cache holds of a page and head (a NaN counts as 0), m = max |k|: the exponent x is the least integer
  * in [-40, 48] with 127 * 2^x >= m (48 if none), bounds row 0 = floor(min k / 2^x), row 1 =
  * ceil(max k / 2^x), clamped to +-127.  A call that writes a page's first slot starts its bounds anew,
- * another widens them.  The tokens of one page must be neighbours (as thin_attn_paged_plan lays
- * them); a page met twice, with another in between, keeps sound keys but may keep the bounds of one
- * of the two runs only.  Of two tokens with one slot, which one stays is not specified. */
+ * another widens them.  The tokens of one page must then be neighbours (as thin_attn_paged_plan
+ * lays them): where another page's or a skipped token stands between two of them, the keys are right but the
+ * bounds may miss one of the two runs.  Of two tokens with one slot either may stay, in part too. */
 typedef struct {
   uint32_t struct_size;
   int32_t device, dtype, cache_dtype, N, H, E, D, page, n_pages;
@@ -436,12 +439,13 @@ THIN_ATTN_API thin_attn_status thin_attn_paged_append(const thin_attn_paged_appe
  * the pages' places in the request, ascending, then -1.
  *
  * E and D multiples of 8 (E4M3: 16) in [8, 256]; pointers and strides multiples of 16 bytes.
+ * out may be q itself (same strides), else they may not overlap.
  * workspace: thin_attn_paged_attention_workspace bytes, 256-byte aligned, not shared by calls that
  * may overlap. */
 typedef struct {
   uint32_t struct_size;
   int32_t device, dtype, cache_dtype, N, R, W, Hq, H, E, D, page, n_pages, window, top, first, last;
-  float scale;               /* <= 0 selects 1/sqrt(E) */
+  float scale;               /* 0 selects 1/sqrt(E); negative: refused */
   const void* q;             /* (N, Hq, E), strides in elements */
   int64_t q_token, q_head;
   const void* k_pages;

@@ -719,3 +719,22 @@ def test_strides_of_axes_of_one_are_free():
     out, lse = torch.empty(4 * E, dtype=torch.bfloat16, device=DEV).as_strided((1, 4, E), (11, E, 1)), torch.empty(1, 4, device=DEV)
     T.paged_attention(q, kp, vp, i32([[0]]), i32([L]), out=out, lse=lse)
     check(out[0], lse[0], q[0], [(kp[0, 0].double(), vp[0, 0].double())], "bf16", "bf16")
+
+
+def test_overlapping_tensors_and_odd_scales_are_refused():
+    kp, vp, _, table, _ = filled([5, 5], 2, 64, 64, 16, "bf16", "bf16")
+    buf, L = torch.zeros(2 * 4 * 64 + 64, dtype=torch.bfloat16, device=DEV), i32([5, 5])
+    q, n = buf[:512].view(2, 4, 64), torch.zeros(1, dtype=torch.int32, device=DEV)
+    row, one = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    for bad in (lambda: T.paged_attention(q, kp, vp, table, L, out=buf[64:].view(2, 4, 64)),
+                lambda: T.paged_attention(q, kp, vp, table, L, out=row.expand(2, 4, 64)),
+                lambda: T.paged_append(row[:, :2], row[:, :2], one, kp, kp),
+                lambda: T.paged_append(row[:, :2], row[:, :2], one, kp[:1].expand(4, -1, -1, -1), vp[:1].expand(4, -1, -1, -1))):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
+    for bad in (lambda: T.paged_plan(L, L, table[:1].expand(2, -1), i32([0]), n, 16, 4),
+                lambda: T.paged_release(L, L, table[:1].expand(2, -1), i32([0]), n, 16),
+                lambda: T.paged_attention(q, kp, vp, table, L, scale=-1.0),
+                lambda: T.paged_attention(q, kp, vp, table, L, scale=float("nan"))):
+        with pytest.raises(T.ThinAttnError, match="EINVAL"):
+            bad()

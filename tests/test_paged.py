@@ -160,3 +160,12 @@ def test_plain_bounds_by_hand():
     assert [PP.exponent(m) for m in (0, 127, 127.5, 1.0, float("inf"))] == [-40, 0, 1, -6, 48]
     assert PP.choose(torch.tensor([[1.0, -1.0]]), torch.tensor([[[0, 0], [1, 1]], [[-5, -5], [0, 0]], [[1, 0], [2, 0]], [[0, 0], [0, 0]]]),
                      [0, 0, 1, 0], 3, 0, 1) == [1, 2, 3]
+
+
+def test_overlapping_table_rows_and_odd_scales_are_refused():
+    for name in ("plan", "release"):
+        refused(name, table_row=7)
+        refused(name, table_row=0)
+        refused(name, table_row=-8)
+    for scale in (-1.0, float("inf"), float("nan")):
+        refused("attention", scale=scale)

@@ -62,6 +62,7 @@ thin_attn_status check_attention(const thin_attn_paged_attention_args* a) {
   if ((int64_t)a->N * a->Hq > kIntMax / 64) return err(THIN_ATTN_EINVAL, "N * Hq = %lld too large", (long long)a->N * a->Hq);
   if ((int64_t)a->W * a->page > kIntMax - 4096) return err(THIN_ATTN_EINVAL, "W * page = %lld too large", (long long)a->W * a->page);
   if (!a->rows && a->N > a->R) return err(THIN_ATTN_EINVAL, "%d tokens without rows over %d requests", a->N, a->R);
+  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return err(THIN_ATTN_EINVAL, "scale=%g", a->scale);
   if (a->window < 0) return err(THIN_ATTN_EINVAL, "window=%d", a->window);
   if (a->top < 0 || a->top > kMaxTop) return err(THIN_ATTN_EINVAL, "top=%d outside 0..%d", a->top, kMaxTop);
   if (a->top) {
@@ -111,6 +112,7 @@ thin_attn_status thin_attn_paged_plan(const thin_attn_paged_plan_args* a, void* 
   if (a->R < 0 || a->W < 0 || a->page < 1 || a->n_pages < 0 || a->max_tokens < 0)
     return err(THIN_ATTN_EINVAL, "R=%d W=%d page=%d n_pages=%d max_tokens=%d", a->R, a->W, a->page, a->n_pages, a->max_tokens);
   if (a->R > kMaxRequests) return err(THIN_ATTN_EUNSUPPORTED, "%d requests, at most %d", a->R, kMaxRequests);
+  if (a->R > 1 && a->table_row < a->W) return err(THIN_ATTN_EINVAL, "table rows of %d ids, %lld apart, overlap", a->W, (long long)a->table_row);
   if (a->R && (!a->lengths || !a->n_new || !a->lengths_out || !a->status)) return err(THIN_ATTN_EINVAL, "null request array");
   if (a->R && a->W && !a->table) return err(THIN_ATTN_EINVAL, "null table");
   if (a->n_pages && !a->free_pages) return err(THIN_ATTN_EINVAL, "null free_pages");
@@ -127,6 +129,7 @@ thin_attn_status thin_attn_paged_release(const thin_attn_paged_release_args* a, 
   if (a->R < 0 || a->W < 0 || a->page < 1 || a->n_pages < 0)
     return err(THIN_ATTN_EINVAL, "R=%d W=%d page=%d n_pages=%d", a->R, a->W, a->page, a->n_pages);
   if (a->R > kMaxRequests) return err(THIN_ATTN_EUNSUPPORTED, "%d requests, at most %d", a->R, kMaxRequests);
+  if (a->R > 1 && a->table_row < a->W) return err(THIN_ATTN_EINVAL, "table rows of %d ids, %lld apart, overlap", a->W, (long long)a->table_row);
   if (a->R == 0) return THIN_ATTN_OK;
   if (!a->keep || !a->lengths || !a->n_free || (a->W && !a->table) || (a->n_pages && !a->free_pages))
     return err(THIN_ATTN_EINVAL, "null array");

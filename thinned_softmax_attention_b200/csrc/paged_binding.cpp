@@ -10,6 +10,7 @@
 // Functions return their tensors, or the status of the C call when it is not 0; wrong arguments raise
 // ValueError.
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,6 +72,10 @@ bool flag(PyObject* o) {
   return v != 0;
 }
 
+bool overlapping(const at::Tensor& x, const at::Tensor& y) {
+  const at::MemOverlapStatus s = at::get_overlap_status(x, y);
+  return s == at::MemOverlapStatus::Full || s == at::MemOverlapStatus::Partial;
+}
 // A stride that is used: that of an axis of one may be any number.
 int64_t stride_of(const at::Tensor& t, int axis) { return t.size(axis) > 1 ? t.stride(axis) : 0; }
 
@@ -304,6 +309,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.device = dev;
     p.N = fits(N, "N");
     p.slots = vector<int64_t>(tensor(a[2], "slots"), "slots", N, at::kLong, dev);
+    if (at::has_internal_overlap(kp) == at::MemOverlap::Yes || at::has_internal_overlap(vp) == at::MemOverlap::Yes || overlapping(kp, vp))
+      refuse("k_pages, v_pages: their rows overlap");
     const Types t = types_of(k, kp);
     const Scales s = scales_of(a[5], a[6], t.cache, pool.H, dev);
     const Bounds b = bounds_of(a[7], a[8], pool, dev);
@@ -407,6 +414,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!out.sizes().equals({N, Hq, D}) || out.scalar_type() != q.scalar_type() || !on(out, dev) || out.stride(2) != 1)
         refuse("out: expected (" + std::to_string(N) + ", " + std::to_string(Hq) + ", " + std::to_string(D) +
                ") of q's type with a contiguous last axis on cuda:" + std::to_string(dev) + ", got " + place(out));
+      const bool same = out.data_ptr() == q.data_ptr() && out.strides().equals(q.strides()) && pool.E == pool.D;
+      if (at::has_internal_overlap(out) == at::MemOverlap::Yes || (!same && overlapping(out, q)))
+        refuse("out: its rows overlap one another or those of q");
     }
     if (a[16] != Py_None) {
       lse = tensor(a[16], "lse");

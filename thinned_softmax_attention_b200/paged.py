@@ -90,7 +90,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     float8_e4m3fn pages hold x / scale[h], rounded to the nearest value, at most 448 in magnitude.
     ``bounds`` = (int8 (n_pages, H, 2, E), int8 (n_pages, H)): the pages' key bounds for
     ``paged_sparse_attention``, widened by the new keys, or started anew where a page's first slot
-    is written; the tokens of one page must then be neighbours, as ``paged_plan`` lays them."""
+    is written; the tokens of one page must then be neighbours, as ``paged_plan`` lays them, with no skipped
+    one between them (to take tokens back, shorten the request: ``paged_release``)."""
     lohi, exps = (None, None) if bounds is None else bounds
     status = _calls().append(k, v, slots, k_pages, v_pages, k_scale, v_scale, lohi, exps)
     if status:
