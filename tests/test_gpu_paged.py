@@ -738,3 +738,28 @@ def test_overlapping_tensors_and_odd_scales_are_refused():
                 lambda: T.paged_attention(q, kp, vp, table, L, scale=float("nan"))):
         with pytest.raises(T.ThinAttnError, match="EINVAL"):
             bad()
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_a_plan_s_tensors_are_tensors_of_their_own(inplace):
+    """They lie in one allocation, and stay right when one is changed, outlives the others or is used in inference mode."""
+    lengths, new, table = i32([3, 0, 30]), i32([2, 5, 40]), torch.full((3, 4), -1, dtype=torch.int32, device=DEV)
+    table[0, 0] = 9
+    want = P.plan([3, 0, 30], [2, 5, 40], table.tolist(), [1, 2, 3], 16, 9)
+    for mode in (torch.enable_grad, torch.no_grad, torch.inference_mode):
+        with mode():
+            args = lengths.clone(), new, table.clone(), i32([1, 2, 3]), i32([3])
+            got = T.paged_plan(*args, 16, 9, inplace=inplace)
+            assert [t.dtype for t in got] == [torch.int32] * 3 + [torch.int64] + [torch.int32] * 3
+            assert (got.lengths is args[0]) == inplace and (got.n_free is args[4]) == inplace
+            assert got.lengths.tolist() == want[0] and got.n_free.tolist() == [len(want[1])]
+            assert got.cu.tolist() == want[2] and got.rows.tolist() == want[4] and got.status.tolist() == want[6]
+            assert got.slots.is_contiguous() and not got.slots.requires_grad
+            got.slots.fill_(-7)
+            got.cu.add_(100)
+            got.status.zero_()
+            assert got.context.tolist() == want[5] and got.rows.tolist() == want[4]
+            rows = got.rows
+            del got, args
+            torch.full((4096,), 5, dtype=torch.int32, device=DEV)
+            assert rows.tolist() == want[4] and rows.clone().add_(1).tolist() == [r + 1 for r in want[4]]

@@ -74,15 +74,15 @@ __device__ __forceinline__ Request request(const thin_attn_paged_plan_args& a, i
   return q;
 }
 
-// Writes slot, request and context of place t.  cu(r): the sums; length(r): the request's length before the
-// step, negative when it was not placed.
+// Writes slot, request and context of place t, below the step's tokens or not (`held`), of the requests
+// lo .. hi - 1.  cu(r): the sums; length(r): the request's length before the step, negative when it was not
+// placed.
 template <typename Cu, typename Length>
-__device__ __forceinline__ void put_token(const thin_attn_paged_plan_args& a, int t, Cu&& cu, Length&& length) {
+__device__ __forceinline__ void put_token(const thin_attn_paged_plan_args& a, int t, bool held, int lo, int hi, Cu&& cu, Length&& length) {
   int64_t slot = -1;
   int row = -1, context = 0;
-  if (t < cu(a.R)) {
-    int lo = 0, hi = a.R;   // the last r with cu[r] <= t
-    while (hi - lo > 1) {
+  if (held) {
+    while (hi - lo > 1) {   // the last r with cu[r] <= t
       const int mid = (lo + hi) >> 1;
       if (cu(mid) <= t) lo = mid; else hi = mid;
     }
@@ -171,14 +171,24 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(thin_attn_paged_plan_arg
   if (tid == 0) *a.n_free_out = (int32_t)(n_free - taken_s);
   if (a.max_tokens <= kFillHere)
     for (int t = tid; t < a.max_tokens; t += threads)
-      put_token(a, t, [&](int r) { return cu_s[r]; }, [&](int r) { return length_s[r]; });
+      put_token(a, t, t < cu_s[a.R], 0, a.R, [&](int r) { return cu_s[r]; }, [&](int r) { return length_s[r]; });
 }
 
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(thin_attn_paged_plan_args a) {
+  // the search begins on every step-th sum, in shared memory: its reads of the others follow one another
+  __shared__ int coarse[kFillThreads];
+  const int t = blockIdx.x * kFillThreads + threadIdx.x, step = (a.R + kFillThreads - 1) / kFillThreads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x * kFillThreads + threadIdx.x;
+  const int tokens = a.cu[a.R];
+  coarse[threadIdx.x] = a.cu[min((int)threadIdx.x * step, a.R)];
+  __syncthreads();
   if (t >= a.max_tokens) return;
-  put_token(a, t, [&](int r) { return a.cu[r]; },
+  int lo = 0, hi = kFillThreads;   // those behind the requests are the step's tokens, above t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (coarse[mid] <= t) lo = mid; else hi = mid;
+  }
+  put_token(a, t, t < tokens, lo * step, min((lo + 1) * step, a.R), [&](int r) { return a.cu[r]; },
             [&](int r) { return a.status[r] ? -1 : a.lengths_out[r] - (a.cu[r + 1] - a.cu[r]); });
 }
 

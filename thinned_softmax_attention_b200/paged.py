@@ -70,7 +70,7 @@ def paged_plan(lengths: torch.Tensor, new: torch.Tensor, table: torch.Tensor, fr
     got = _calls().plan(lengths, new, table, free, n_free, page, max_tokens, inplace)
     if type(got) is int:
         _raise(got)
-    return PagedPlan(*got)
+    return PagedPlan._make(got)
 
 
 def paged_release(keep: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor, free: torch.Tensor,
