@@ -356,8 +356,8 @@ THIN_ATTN_API thin_attn_status thin_attn_halve_noalloc(int dtype, const void* K,
  * request r with cu[r] <= t < cu[r + 1], cu the prefix sums of max(n_new, 0):
  *   slots[t], rows[t] = r, context[t] = the tokens of r up to and with t (t's position + 1)
  * and -1, -1, 0 for tokens of requests that were not placed and for t >= cu[R].
- * lengths_out and n_free_out may be lengths and n_free themselves.  At most 16384 requests; rows of the
- * table may not overlap. */
+ * lengths_out and n_free_out may be lengths and n_free themselves.  At most 16384 requests and 2^30 - 1
+ * max_tokens; rows of the table may not overlap. */
 typedef struct {
   uint32_t struct_size;
   int32_t device, R, W, page, n_pages, max_tokens, reserved;   /* n_pages: entries of free_pages */

@@ -169,3 +169,8 @@ def test_overlapping_table_rows_and_odd_scales_are_refused():
         refused(name, table_row=-8)
     for scale in (-1.0, float("inf"), float("nan")):
         refused("attention", scale=scale)
+
+
+def test_more_places_than_a_plan_counts_are_refused():
+    refused("plan", max_tokens=2 ** 31 - 1)
+    refused("plan", max_tokens=2 ** 30)

@@ -112,6 +112,7 @@ thin_attn_status thin_attn_paged_plan(const thin_attn_paged_plan_args* a, void* 
   if (a->R < 0 || a->W < 0 || a->page < 1 || a->n_pages < 0 || a->max_tokens < 0)
     return err(THIN_ATTN_EINVAL, "R=%d W=%d page=%d n_pages=%d max_tokens=%d", a->R, a->W, a->page, a->n_pages, a->max_tokens);
   if (a->R > kMaxRequests) return err(THIN_ATTN_EUNSUPPORTED, "%d requests, at most %d", a->R, kMaxRequests);
+  if (a->max_tokens > kIntMax / 2) return err(THIN_ATTN_EUNSUPPORTED, "max_tokens=%d, at most %lld", a->max_tokens, (long long)kIntMax / 2);
   if (a->R > 1 && a->table_row < a->W) return err(THIN_ATTN_EINVAL, "table rows of %d ids, %lld apart, overlap", a->W, (long long)a->table_row);
   if (a->R && (!a->lengths || !a->n_new || !a->lengths_out || !a->status)) return err(THIN_ATTN_EINVAL, "null request array");
   if (a->R && a->W && !a->table) return err(THIN_ATTN_EINVAL, "null table");

@@ -9,7 +9,7 @@
 // dependent latencies (lengths, sums, search, page id), so one CTA takes it all while the tokens are few,
 // and a second launch spreads the tokens over the GPU when they are many.  Both sums are taken at
 // once, as if every token had room; only where one has not are the pages summed again.
-// B200: 64 requests of one token 3.5 us, 512 of them 5.4, 65536 tokens of 512 requests 13 us.
+// B200: 64 requests of one token 3.5 us, 512 of them 5.4, 65536 tokens of 512 requests 12 us.
 #include "paged.h"
 
 namespace thin {
@@ -18,9 +18,9 @@ namespace {
 
 // Of the first launch; 64 requests with 256 threads 3.6 us, with 1024 4.6.
 constexpr int kThreads = 1024, kFewThreads = 256;
-// Tokens that the first launch places itself: alone and with the second launch 3.6 and 5.8 us for 64 tokens,
-// 7.0 and 7.2 for 4096, 8.5 and 7.7 for 8192, 67 and 13 for 65536.
-constexpr int kFillHere = 4096;
+// Tokens that the first launch places itself: alone and with the second launch, 64 requests 3.6 and 5.8 us for 64
+// tokens, 6.4 and 7.1 for 2048, 7.5 and 7.2 for 4096; 512 requests 6.7 and 6.7 for 2048, 7.9 and 6.5 for 4096.
+constexpr int kFillHere = 2048;
 constexpr int kFillThreads = 256;
 constexpr int kOwnPages = 2;                        // fresh pages that a request's thread enters itself
 
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(thin_attn_paged_plan_arg
   if (__syncthreads_or(many)) {
     // the e-th page taken goes to the last request with base <= e (one that takes none shares its base with
     // the next; behind the last placed request no base is below the pages taken)
-    for (int e = tid; e < taken_s; e += threads) {
+    for (int64_t e = tid; e < taken_s; e += threads) {
       int lo = 0, hi = a.R;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
