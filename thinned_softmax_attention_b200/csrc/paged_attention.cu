@@ -28,6 +28,10 @@
 // fp32 caches use the tf32 products (m16n8k8) with every operand as the sum of two tf32 numbers,
 // (a_hi + a_lo)(b_hi + b_lo), good to 2^-22.  The upper rows of the tile carry a_lo, so that takes two products.
 //
+// The tensor cores cut their sums, they do not round them: a sum that runs on in an accumulator drifts towards
+// zero, in fp32 by 2.5e-4 over 65536 keys.  So a product of fp32 begins at zero, and stage is added to stage (columns
+// of a score: 32 to 32) by ordinary additions.
+//
 // These are the 16-row products on purpose: tcgen05 tiles have 64 or 128 rows, of which G would fill a few,
 // and their operands pass through shared memory in fixed layouts, P included.  The tensor pipe is no bound here
 // (24% busy at e4m3, the densest case).
@@ -501,11 +505,20 @@ struct Tf32Tile {
 
   __device__ __forceinline__ void step(const PagedAttn& p, uint32_t ks, uint32_t vs, uint32_t seen, int lane, float* sm) {
     const int r = lane >> 2, c = lane & 3;
-    float s0[4] = {}, s1[4] = {};
+    // products of the keys' leading parts and of their lower ones, 32 columns at a time (kChain)
+    float s0[4] = {}, s1[4] = {}, s[4] = {};
+    constexpr int kChain = 2;
     const uint32_t ka = ks + r * RB + ((c ^ swizzle(r)) << 4);   // column r of S is key r
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
       if (j * 16 >= p.a.E) break;
+      if (j && j % kChain == 0) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          s[y] += s0[y];
+          s0[y] = 0.f;
+        }
+      }
       const Split k = split4(lds16((ka ^ ((j & 1) << 6)) + (j >> 1) * 128));
       uint32_t h[4], w[4];
       if constexpr (kQueryInSmem) {
@@ -536,29 +549,19 @@ struct Tf32Tile {
     float z[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      z[u] = (s0[u] + (s0[2 + u] + (s1[u] + s1[2 + u]))) * sc;
+      z[u] = ((s[u] + s0[u]) + ((s[2 + u] + s0[2 + u]) + (s1[u] + s1[2 + u]))) * sc;
       if (!((seen >> (2 * c + u)) & 1)) z[u] = -INFINITY;
     }
     float mx = fmaxf(z[0], z[1]);
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-    if (__any_sync(0xffffffffu, mn != m)) {
-      const float f = ex2(m - ref);
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < VI; ++i)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          o[i][y][0] *= f;
-          o[i][y][1] *= f;
-          o[i][y][2] *= f;
-          o[i][y][3] *= f;
-        }
-    }
+    const float f = ex2(m - ref);
     m = mn;
-    const float p0 = ex2(z[0] - ref), p1 = ex2(z[1] - ref);
-    l += p0 + p1;
+    // weights of 22 bits, which two tf32 numbers hold; the sum takes the same
+    const float p0 = __uint_as_float(__float_as_uint(ex2(z[0] - ref)) & 0xFFFFFFFCu);
+    const float p1 = __uint_as_float(__float_as_uint(ex2(z[1] - ref)) & 0xFFFFFFFCu);
+    l = fmaf(l, f, p0 + p1);
     const uint32_t h0 = __float_as_uint(p0) & 0xFFFFE000u, h1 = __float_as_uint(p1) & 0xFFFFE000u;
     // P's slots c and c + 4 are keys 2 c and 2 c + 1
     const uint32_t a[4] = {h0, __float_as_uint(p0 - __uint_as_float(h0)), h1, __float_as_uint(p1 - __uint_as_float(h1))};
@@ -569,8 +572,11 @@ struct Tf32Tile {
       const Split v0 = split4(lds16(va + i * 128)), v1 = split4(lds16((va ^ 64) + RB + i * 128));
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        mma_tf32(o[i][y], a, v0.hi[y], v1.hi[y]);
-        mma_tf32(o[i][y], a, v0.lo[y], v1.lo[y]);
+        float t[4] = {};
+        mma_tf32(t, a, v0.lo[y], v1.lo[y]);
+        mma_tf32(t, a, v0.hi[y], v1.hi[y]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[i][y][x] = fmaf(o[i][y][x], f, t[x]);
       }
     }
   }
