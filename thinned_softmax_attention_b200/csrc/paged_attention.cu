@@ -29,8 +29,9 @@
 // (a_hi + a_lo)(b_hi + b_lo), good to 2^-22.  The upper rows of the tile carry a_lo, so that takes two products.
 //
 // The tensor cores cut their sums, they do not round them: a sum that runs on in an accumulator drifts towards
-// zero, in fp32 by 2.5e-4 over 65536 keys.  So a product of fp32 begins at zero, and stage is added to stage (columns
-// of a score: 32 to 32) by ordinary additions.
+// zero, by 2.5e-4 over 65536 keys of a CTA in fp32, by 1e-4 in the 16-bit types.  So the products of P and V begin at zero
+// every 16 keys (fp32: 8), as those of fp32's scores do every 32 columns, and are added up by ordinary additions, which
+// take the rescaling with the maximum along.  That costs 3% (e4m3) or nothing seen (16 bits; 16 rows of width 256: -8%).
 //
 // These are the 16-row products on purpose: tcgen05 tiles have 64 or 128 rows, of which G would fill a few,
 // and their operands pass through shared memory in fixed layouts, P included.  The tensor pipe is no bound here
@@ -100,6 +101,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -144,6 +148,7 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 template <typename T, typename C, int HD, int ROWS_>
 struct MmaTile {
   static constexpr int ROWS = ROWS_;
+  static constexpr int COLS = ROWS == 8 && HD > 64 ? 128 : 64;   // columns joined at a time
   static constexpr int kSmem = 0;
   static constexpr bool k8 = sizeof(C) == 1;
   using M = typename std::conditional<k8, __half, T>::type;   // the products' type
@@ -193,7 +198,12 @@ struct MmaTile {
     }
   }
 
-  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float*) {
+  // bf16 queries as fp16 by way of shared memory: 16-byte loads leave them in neighbouring registers, where conversions
+  // spilled 64 of them (40 e4m3 requests of width 256: 75 us, without 120; of width 128, which does not spill, 43.0, without 42.0)
+  static constexpr bool kByShared = HD == 256 && ROWS == 8;
+  // own: the warp's part of the merge buffer, which no other warp uses between two pairs' ends
+  __device__ __forceinline__ void reset(const PagedAttn& p, int n, int row0, int rows, float scale, int lane, float* own) {
+    static_assert(!kByShared || KJ * QW * 128 <= ROWS * COLS * 4, "");
     if constexpr (!kAhead) fetch(p, n, row0, rows, lane);
 #pragma unroll
     for (int x = 0; x < ROWS / 8; ++x) {
@@ -217,7 +227,22 @@ struct MmaTile {
 #pragma unroll
           for (int y = 0; y < QW; ++y) {
             const float2 f = unpack2<T>(next[j][x][y]);
-            q[j][x][y] = pack2<__half>(f.x * pow2f(up), f.y * pow2f(up));
+            next[j][x][y] = pack2<__half>(f.x * pow2f(up), f.y * pow2f(up));
+          }
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(own) + lane * 16;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+#pragma unroll
+          for (int y = 0; y < QW; y += 4) {
+            uint4 u = make_uint4(next[j][x][y], next[j][x][y + 1], next[j][x][y + 2], next[j][x][y + 3]);
+            if constexpr (kByShared) {
+              sts16(at + (j * QW + y) * 128, u);
+              u = lds16(at + (j * QW + y) * 128);
+            }
+            q[j][x][y] = u.x;
+            q[j][x][y + 1] = u.y;
+            q[j][x][y + 2] = u.z;
+            q[j][x][y + 3] = u.w;
           }
         sc[x] = scale * pow2f(-up);
       } else {
@@ -289,7 +314,6 @@ struct MmaTile {
     }
     uint32_t hi[2][NB][2], lo[2][NB][2];   // [x][b][t]
     float f[2];
-    bool grown = false;
 #pragma unroll
     for (int x = 0; x < ROWS / 8; ++x) {
       float mx = -INFINITY;
@@ -301,7 +325,6 @@ struct MmaTile {
       const float mn = fmaxf(m[x], mx);
       const float ref = mn == -INFINITY ? 0.f : mn;
       f[x] = ex2(m[x] - ref);
-      grown |= mn != m[x];
       m[x] = mn;
       float sum = 0.f;
 #pragma unroll
@@ -319,18 +342,11 @@ struct MmaTile {
         }
       l[x] = l[x] * f[x] + sum;
     }
-    if (__any_sync(0xffffffffu, grown)) {
-      const float f1 = ROWS == 16 ? f[ROWS / 8 - 1] : f[0];
+    const float f1 = ROWS == 16 ? f[ROWS / 8 - 1] : f[0];
+    auto add = [&](float (&x)[4], const float (&t)[4], int b) {
 #pragma unroll
-      for (int i = 0; i < VI; ++i)
-#pragma unroll
-        for (int y = 0; y < DC; ++y) {
-          o[i][y][0] *= f[0];
-          o[i][y][1] *= f[0];
-          o[i][y][2] *= f1;
-          o[i][y][3] *= f1;
-        }
-    }
+      for (int z = 0; z < 4; ++z) x[z] = b ? x[z] + t[z] : fmaf(x[z], z < 2 ? f[0] : f1, t[z]);
+    };
     const uint32_t va = vs + 4 * c * RB + ((r ^ (c << 1)) << 4);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -360,16 +376,21 @@ struct MmaTile {
               uint32_t p0[2], p1[2];
               widen4(b0, p0[0], p0[1]);
               widen4(b1, p1[0], p1[1]);
-              mma<M>(o[i][4 * w + 2 * y], a, p0[0], p1[0]);
-              mma<M>(o[i][4 * w + 2 * y + 1], a, p0[1], p1[1]);
+              float t0[4] = {}, t1[4] = {};
+              mma<M>(t0, a, p0[0], p1[0]);
+              mma<M>(t1, a, p0[1], p1[1]);
+              add(o[i][4 * w + 2 * y], t0, b);
+              add(o[i][4 * w + 2 * y + 1], t1, b);
             }
           } else {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const uint32_t sel = y ? 0x7632 : 0x5410;
               const uint32_t b0 = __byte_perm(v[0][w], v[1][w], sel), b1 = __byte_perm(v[2][w], v[3][w], sel);
-              mma<M>(o[i][2 * w + y], a, b0, b1);
-              if constexpr (kSplit && ROWS == 16) mma<M>(o[i][2 * w + y], a2, b0, b1);
+              float t[4] = {};
+              if constexpr (kSplit && ROWS == 16) mma<M>(t, a2, b0, b1);
+              mma<M>(t, a, b0, b1);
+              add(o[i][2 * w + y], t, b);
             }
           }
         }
@@ -390,7 +411,6 @@ struct MmaTile {
     }
   }
   // Columns [COLS part, COLS part + COLS) of o into dst (ROWS x COLS).
-  static constexpr int COLS = ROWS == 8 && HD > 64 ? 128 : 64;
   static __device__ __forceinline__ int place(int g, int col) {   // float4 `col` of row g: quarter-warps meet every bank once
     return g * (COLS / 4) + (col ^ ((col >> 3) & 3) ^ ((g & 1) << (k8 ? 2 : 1)));
   }
@@ -855,7 +875,8 @@ __global__ void __launch_bounds__(WARPS * 32, PER_SM) attention_kernel(PagedAttn
     const int h = me.which() / tiles, g0 = (me.which() % tiles) * ROWS, rows = min(ROWS, G - g0);
     if (me.first()) {
       slot = s > 0;
-      t.reset(p, me.n, h * G + g0, rows, p.scale_log2e * (a.k_scale ? a.k_scale[h] : 1.f), lane, scratch);
+      t.reset(p, me.n, h * G + g0, rows, p.scale_log2e * (a.k_scale ? a.k_scale[h] : 1.f), lane,
+              Tile::kSmem ? scratch : (float*)(merge + warp * ROWS * (Tile::COLS / 4)));
     }
     if (s + 1 < filled && meta[warp][(s + 1) % STAGES].first()) fetch(meta[warp][(s + 1) % STAGES]);
     const uint32_t ks = ring + st * S::kStage;
