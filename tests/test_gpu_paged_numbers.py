@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import thinned_softmax_attention_b200 as T
-from tests.test_gpu_paged import DEV, TYPES, i32, rnd
+from tests.test_gpu_paged import DEV, TYPES, check, i32, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,18 @@ def test_very_long_sums_of_16_bit_types_do_not_drift(dtype, cache, width, G, key
     out = T.paged_attention(q, kp, vp, table, i32([keys] * tokens), k_scale=one, v_scale=one).view(tokens, H, G, width)
     off = ((out.double() - c.double()[None, :, None]) / c.double()[None, :, None]).abs().max()
     assert float(off) == 0.0, float(off)
+
+
+@pytest.mark.parametrize("G", [4, 8, 12, 16])
+def test_weights_against_an_8_bit_cache_keep_more_than_16_bits(G):
+    """Two keys of nearly equal weight and opposite values: what a weight loses is the output's error.  A weight in one
+    fp16 number would be off by up to 2^-12, the tolerance takes it as good to 2^-16 (its two parts: 2^-22)."""
+    E, page = 64, 16
+    kp, vp = (torch.zeros(1, 1, page, E, device=DEV) for _ in range(2))
+    kp[0, 0, 0, 0], kp[0, 0, 1, 0], vp[0, 0, 0], vp[0, 0, 1] = 1.0, -1.0, 1.0, -1.0
+    one, q = torch.ones(1, device=DEV), torch.zeros(8, G, E, dtype=torch.float16, device=DEV)
+    q[..., 0] = (torch.arange(1, 8 * G + 1, device=DEV) * 1.37e-4).view(8, G).half()
+    out, lse = T.paged_attention(q, kp.to(TYPES["e4m3"]), vp.to(TYPES["e4m3"]), i32([[0]] * 8), i32([2] * 8), scale=1.0, k_scale=one,
+                                 v_scale=one, return_lse=True)
+    for n in range(8):   # held to the 16-bit caches' bound of a weight
+        check(out[n], lse[n], q[n], [(kp[0, 0, :2], vp[0, 0, :2])], "fp16", "fp16", 1.0)

@@ -23,7 +23,7 @@
 // lane (r, c) holds the columns of keys 4 c .. 4 c + 3, reads those four rows of V as 16-byte pieces
 // (of d = DC (r + 8 i) ..) and pairs them up with byte permutations.  No transposing load, no shuffle but
 // the row maximum.  G <= 8 leaves the tile's upper 8 rows free: they carry P's rounding error, so P
-// keeps 16 bits and more at no cost; G <= 16 issues that product separately (16-bit caches).
+// keeps 16 bits and more at no cost; G <= 16 issues that product separately.
 //
 // fp32 caches use the tf32 products (m16n8k8) with every operand as the sum of two tf32 numbers,
 // (a_hi + a_lo)(b_hi + b_lo), good to 2^-22.  The upper rows of the tile carry a_lo, so that takes two products.
@@ -156,7 +156,9 @@ struct MmaTile {
   static constexpr int DC = 16 / (int)sizeof(C);              // elements of a 16-byte piece
   static constexpr int KJ = RB / 64, VI = RB / 128;           // pieces of K and V per lane and row
   static constexpr int QW = DC / 2;                           // words of Q per piece
-  static constexpr bool kSplit = !k8 || ROWS == 8;            // P as two numbers
+  // P as two numbers.  One is enough for 16 bf16 rows against e4m3: off by 2^-12 at most, an eighth of what the output is
+  // rounded by; the second product would take 252 us to 299 (40 requests of 32768 keys; fp16 282 to 320)
+  static constexpr bool kSplit = !k8 || ROWS == 8 || std::is_same<T, __half>::value;
   static constexpr int kKeys = RB <= 128 ? 32 : 16;           // keys of a stage: short rows, twice as many for the same overhead
   static constexpr int NB = kKeys / 16;                       // products' blocks of 16 keys
   // fp16 weights are lifted by 2^14: without that those below 2^-14 of the largest lose bits, and a long
@@ -377,6 +379,10 @@ struct MmaTile {
               widen4(b0, p0[0], p0[1]);
               widen4(b1, p1[0], p1[1]);
               float t0[4] = {}, t1[4] = {};
+              if constexpr (kSplit && ROWS == 16) {
+                mma<M>(t0, a2, p0[0], p1[0]);
+                mma<M>(t1, a2, p0[1], p1[1]);
+              }
               mma<M>(t0, a, p0[0], p1[0]);
               mma<M>(t1, a, p0[1], p1[1]);
               add(o[i][4 * w + 2 * y], t0, b);
