@@ -428,6 +428,8 @@ THIN_ATTN_API thin_attn_status thin_attn_paged_append(const thin_attn_paged_appe
  * length of zero, pages that all lie outside the pool) gets zeros and -inf; one whose row lies
  * outside [0, R) is padding, and its rows of out, lse and pages_out stay as they were.  A key on a page
  * outside the pool is not seen.  Lengths are clamped to [0, W * page].
+ * A key whose score is -inf has no weight (a row with no other key: zeros and -inf); a score that is NaN or +inf makes
+ * its query row's out and lse NaN.
  *
  * top > 0 selects pages: token n and key head h attend to min(top, P) of the request's P pages: the
  * first `first`, the last `last`, and those of the highest score (ties: the lowest index), P = the

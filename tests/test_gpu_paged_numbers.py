@@ -1,9 +1,11 @@
 """Paged operators where numbers are hardest: long sums, infinities, ends of the types' ranges, values next to a border."""
+import math
+
 import pytest
 import torch
 
 import thinned_softmax_attention_b200 as T
-from tests.test_gpu_paged import DEV, TYPES, check, i32, rnd
+from tests.test_gpu_paged import DEV, TYPES, check, filled, i32, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +63,20 @@ def test_weights_against_an_8_bit_cache_keep_more_than_16_bits(G):
                                  v_scale=one, return_lse=True)
     for n in range(8):   # held to the 16-bit caches' bound of a weight
         check(out[n], lse[n], q[n], [(kp[0, 0, :2], vp[0, 0, :2])], "fp16", "fp16", 1.0)
+
+
+@pytest.mark.parametrize("L", [1, 40, 5000])
+@pytest.mark.parametrize("dtype,G", [("fp32", 4), ("fp32", 12), ("bf16", 4), ("bf16", 12), ("fp16", 4), ("fp16", 12)])
+def test_infinite_keys_have_no_weight(dtype, G, L):
+    """A visible key whose score is -inf counts as none, whatever the bits of the query."""
+    H, E, page = 2, 64, 16
+    kp, vp, _, table, held = filled([L], H, E, E, page, dtype, dtype, 51)
+    q = rnd(torch.Generator(DEV).manual_seed(52), 1, H * G, E)
+    q[0, :, 5] = torch.tensor([1.0, 0.3, 1.1, 2.0], device=DEV).repeat(H * G // 4)
+    q = q.to(TYPES[dtype])
+    hidden = [j for j in {0, 7, 17, L - 1} if j < L]
+    for j in hidden:
+        kp[int(table[0, j // page]), :, j % page, 5] = -math.inf
+    keep = [j for j in range(L) if j not in hidden]
+    out, lse = T.paged_attention(q, kp, vp, table, i32([L]), return_lse=True)
+    check(out[0], lse[0], q[0], [(held[0][0][h, keep], held[0][1][h, keep]) for h in range(H)], dtype, dtype)

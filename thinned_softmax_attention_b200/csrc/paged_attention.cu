@@ -110,6 +110,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A sum of leading parts and what their lower parts add: nothing where it is infinite, since a lower part of 0
+// or of the other sign makes a NaN of an infinite factor.
+__device__ __forceinline__ float with_rest(float lead, float rest) { return fabsf(lead) == INFINITY ? lead : lead + rest; }
+
 template <typename M>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   uint32_t r;
@@ -575,7 +579,7 @@ struct Tf32Tile {
     float z[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      z[u] = ((s[u] + s0[u]) + ((s[2 + u] + s0[2 + u]) + (s1[u] + s1[2 + u]))) * sc;
+      z[u] = with_rest(s[u] + s0[u], (s[2 + u] + s0[2 + u]) + (s1[u] + s1[2 + u])) * sc;
       if (!((seen >> (2 * c + u)) & 1)) z[u] = -INFINITY;
     }
     float mx = fmaxf(z[0], z[1]);
