@@ -430,6 +430,8 @@ THIN_ATTN_API thin_attn_status thin_attn_paged_append(const thin_attn_paged_appe
  * outside the pool is not seen.  Lengths are clamped to [0, W * page].
  * A key whose score is -inf has no weight (a row with no other key: zeros and -inf); a score that is NaN or +inf makes
  * its query row's out and lse NaN.
+ * An infinite value gives an infinity in its column of out; infinities of both signs there, or one whose weight
+ * underflows (below 2^-126 of the row's largest; in fp16 2^-38), NaN.
  *
  * top > 0 selects pages: token n and key head h attend to min(top, P) of the request's P pages: the
  * first `first`, the last `last`, and those of the highest score (ties: the lowest index), P = the

@@ -80,3 +80,29 @@ def test_infinite_keys_have_no_weight(dtype, G, L):
     keep = [j for j in range(L) if j not in hidden]
     out, lse = T.paged_attention(q, kp, vp, table, i32([L]), return_lse=True)
     check(out[0], lse[0], q[0], [(held[0][0][h, keep], held[0][1][h, keep]) for h in range(H)], dtype, dtype)
+
+
+@pytest.mark.parametrize("L", [40, 5000])
+@pytest.mark.parametrize("dtype,G", [("fp32", 4), ("fp32", 12), ("bf16", 4), ("bf16", 12), ("fp16", 4), ("fp16", 12)])
+def test_infinite_values(dtype, G, L):
+    """A column with an infinite value is that infinity, with both infinities NaN; the other columns are as without.  Key 2
+    of the longer request has weights from 2^-22 down to below 2^-38 of the largest, where an fp16 weight may be none."""
+    H, E, page = 2, 64, 16
+    kp, vp, _, table, held = filled([L], H, E, E, page, dtype, dtype, 53)
+    q = rnd(torch.Generator(DEV).manual_seed(54), 1, H * G, E).to(TYPES[dtype])
+    place = lambda j: (int(table[0, j // page]), slice(None), j % page)
+    if L > 40:
+        q[0, :, 7] = 8.0
+        kp[place(2)][:, 7] = held[0][0][:, 2, 7] = -20.0
+    for j, d, x in ([(2, 1, math.inf)] if L > 40 else []) + [(3, 1, math.inf), (20, 9, -math.inf), (L - 1, 63, math.inf),
+                                                             (L - 2, 63, math.inf), (8, 30, math.inf), (30, 30, -math.inf)]:
+        vp[place(j)][:, d] = x
+        held[0][1][:, j, d] = 0.0
+    out, lse = T.paged_attention(q, kp, vp, table, i32([L]), return_lse=True)
+    z = torch.einsum("hge,hse->hgs", q[0].double().view(H, G, E), held[0][0]).flatten(0, 1) / math.sqrt(E)
+    none = (z[:, 2] - z.amax(-1) < -38 * math.log(2)) & torch.tensor(dtype == "fp16" and L > 40, device=DEV)
+    assert ((out[0, :, 1] == math.inf) | (none & torch.isnan(out[0, :, 1]))).all() and not none.all()
+    assert (out[0, :, 9] == -math.inf).all() and (out[0, :, 63] == math.inf).all()
+    assert torch.isnan(out[0, :, 30]).all()
+    rest = [d for d in range(E) if d not in (1, 9, 30, 63)]
+    check(out[0][:, rest], lse[0], q[0], [(held[0][0][h], held[0][1][h][:, rest]) for h in range(H)], dtype, dtype)
