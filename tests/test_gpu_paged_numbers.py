@@ -106,3 +106,15 @@ def test_infinite_values(dtype, G, L):
     assert torch.isnan(out[0, :, 30]).all()
     rest = [d for d in range(E) if d not in (1, 9, 30, 63)]
     check(out[0][:, rest], lse[0], q[0], [(held[0][0][h], held[0][1][h][:, rest]) for h in range(H)], dtype, dtype)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-50])
+def test_a_scale_of_zero_is_refused(scale):
+    """The C entry reads 0 as 1 / sqrt(E): a zero that a caller gives may not turn into that."""
+    kp, vp, _, table, _ = filled([5], 1, 64, 64, 16, "bf16", "bf16")
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    b = (torch.zeros(4, 1, 2, 64, dtype=torch.int8, device=DEV), torch.zeros(4, 1, dtype=torch.int8, device=DEV))
+    for call in (lambda: T.paged_attention(q, kp, vp, table, i32([5]), scale=scale),
+                 lambda: T.paged_sparse_attention(q, kp, vp, table, i32([5]), b, 2, scale=scale)):
+        with pytest.raises(ValueError, match="scale"):
+            call()

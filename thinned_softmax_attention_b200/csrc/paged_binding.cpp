@@ -387,6 +387,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[6] != Py_None) {
       p.scale = (float)PyFloat_AsDouble(a[6]);
       if (PyErr_Occurred()) throw Refused();
+      if (p.scale == 0.f) refuse("scale=0 (or a number that rounds to 0 in fp32): the C entry would take it for 1/sqrt(E)");
     }
     const Scales s = scales_of(a[7], a[8], t.cache, pool.H, dev);
     p.k_scale = s.k;
