@@ -118,3 +118,17 @@ def test_a_scale_of_zero_is_refused(scale):
                  lambda: T.paged_sparse_attention(q, kp, vp, table, i32([5]), b, 2, scale=scale)):
         with pytest.raises(ValueError, match="scale"):
             call()
+
+
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("size", [-125, -110, -60, 0, 100, 120, 124])
+def test_bf16_queries_of_any_size_against_an_8_bit_cache(size, G):
+    """Queries near the ends of bf16's range, keys scaled the other way: the scores are ordinary numbers."""
+    L, H, E, page = 300, 2, 64, 16
+    kp, vp, (ks, vs), table, held = filled([L], H, E, E, page, "bf16", "e4m3", 55)
+    q = (rnd(torch.Generator(DEV).manual_seed(56), 1, H * G, E) * 2.0 ** size).bfloat16()
+    assert torch.isfinite(q).all()
+    K = [held[0][0][h] / ks[h].double() * 2.0 ** (-size - 5) for h in range(H)]
+    ks.fill_(2.0 ** (-size - 5))
+    out, lse = T.paged_attention(q, kp, vp, table, i32([L]), k_scale=ks, v_scale=vs, return_lse=True)
+    check(out[0], lse[0], q[0], [(K[h], held[0][1][h]) for h in range(H)], "bf16", "e4m3")
