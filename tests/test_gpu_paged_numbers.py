@@ -1,4 +1,5 @@
 """Paged operators where numbers are hardest: long sums, infinities, ends of the types' ranges, values next to a border."""
+import io
 import math
 
 import pytest
@@ -132,3 +133,12 @@ def test_bf16_queries_of_any_size_against_an_8_bit_cache(size, G):
     ks.fill_(2.0 ** (-size - 5))
     out, lse = T.paged_attention(q, kp, vp, table, i32([L]), k_scale=ks, v_scale=vs, return_lse=True)
     check(out[0], lse[0], q[0], [(K[h], held[0][1][h]) for h in range(H)], "bf16", "e4m3")
+
+
+def test_a_plan_can_be_saved():
+    plan = T.paged_plan(i32([3, 0]), i32([2, 5]), i32([[9, -1], [-1, -1]]), i32([1, 2, 3]), i32([3]), 16, 9)
+    buf = io.BytesIO()
+    torch.save(tuple(plan), buf)
+    buf.seek(0)
+    for a, b in zip(plan, torch.load(buf)):
+        assert torch.equal(a, b)

@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
+#include <vector>
 
 #include "thin_attn.h"
 
@@ -244,20 +245,13 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("table of " + std::to_string(t.R) + " rows, " + std::to_string(R) + " requests, page=" + std::to_string(p.page) + ", max_tokens=" +
              std::to_string(p.max_tokens) + ": expected a row per request, page >= 1, max_tokens >= 0");
     const int64_t T = p.max_tokens;
-    // the outputs in one allocation, slots (int64) first; tensors over its parts are put together here (a call 6.0 us;
-    // with slots allocated apart 7.0, and the others' tensors split off by torch 7.7)
-    const int64_t sizes[6] = {T, T, R + 1, R, R, 1}, ints = 2 * T + 2 * R + 1 + (inplace ? 0 : R + 1);
-    const at::Tensor all = at::empty({T + (ints + 1) / 2}, lengths.options().dtype(at::kLong));
-    auto view = [&](caffe2::TypeMeta type, int64_t begin, int64_t n) {
-      auto impl = c10::make_intrusive<at::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(all.storage()), all.key_set(), type);
-      impl->set_storage_offset(begin);
-      impl->set_sizes_contiguous(at::IntArrayRef(&n, 1));
-      return at::Tensor(std::move(impl));
-    };
-    const at::Tensor slots = view(all.dtype(), 0, T);
-    at::Tensor part[6];
-    int64_t begin = 2 * T;
-    for (int i = 0; i < (inplace ? 4 : 6); begin += sizes[i++]) part[i] = view(lengths.dtype(), begin, sizes[i]);
+    // two allocations, the int32 outputs being parts of one (7.2 us a call; with all in one storage of two types, which
+    // torch.save refuses, 5.9)
+    const at::Tensor slots = at::empty({T}, lengths.options().dtype(at::kLong));
+    std::vector<int64_t> sizes = {T, T, R + 1, R};
+    if (!inplace) sizes.insert(sizes.end(), {R, 1});
+    const std::vector<at::Tensor> part =
+        at::empty({2 * T + 2 * R + 1 + (inplace ? 0 : R + 1)}, lengths.options()).split_with_sizes(sizes);
     const at::Tensor& lengths_out = inplace ? lengths : part[4];
     const at::Tensor& n_free_out = inplace ? n_free : part[5];
     p.slots = (int64_t*)slots.data_ptr();
