@@ -142,3 +142,22 @@ def test_a_plan_can_be_saved():
     buf.seek(0)
     for a, b in zip(plan, torch.load(buf)):
         assert torch.equal(a, b)
+
+
+def test_a_gradient_is_not_dropped_in_silence():
+    kp, vp, _, table, _ = filled([5], 1, 64, 64, 16, "bf16", "bf16")
+    b = (torch.zeros(4, 1, 2, 64, dtype=torch.int8, device=DEV), torch.zeros(4, 1, dtype=torch.int8, device=DEV))
+    q, k = (torch.zeros(1, n, 64, dtype=torch.bfloat16, device=DEV) for n in (2, 1))
+    slot, one = torch.zeros(1, dtype=torch.int64, device=DEV), torch.ones(1, device=DEV)
+    leaf = lambda x: x.clone().requires_grad_()
+    for call in (lambda: T.paged_attention(leaf(q), kp, vp, table, i32([5])), lambda: T.paged_attention(q, leaf(kp), vp, table, i32([5])),
+                 lambda: T.paged_attention(q, kp, leaf(vp), table, i32([5])), lambda: T.paged_attention(leaf(q) * 2, kp, vp, table, i32([5])),
+                 lambda: T.paged_sparse_attention(leaf(q), kp, vp, table, i32([5]), b, 2),
+                 lambda: T.paged_attention(q, kp, vp, table, i32([5]), out=leaf(q)),
+                 lambda: T.paged_attention(q, kp, vp, table, i32([5]), lse=torch.zeros(1, 2, device=DEV, requires_grad=True)),
+                 lambda: T.paged_attention(q, kp.to(TYPES["e4m3"]), vp.to(TYPES["e4m3"]), table, i32([5]), k_scale=leaf(one), v_scale=one),
+                 lambda: T.paged_append(leaf(k), k, slot, kp, vp), lambda: T.paged_append(k, leaf(k), slot, kp, vp)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad():
+            call()

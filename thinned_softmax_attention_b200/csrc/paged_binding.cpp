@@ -11,6 +11,7 @@
 // ValueError.
 #include <ATen/ATen.h>
 #include <ATen/MemoryOverlap.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -144,6 +145,13 @@ Types types_of(const at::Tensor& x, const at::Tensor& pages) {
   return t;
 }
 
+// The operators have no gradients: a tensor that is to get one is refused, its gradient not dropped.
+void no_gradient(std::initializer_list<const at::Tensor*> ts) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (const at::Tensor* t : ts)
+    if (t->requires_grad()) refuse("a tensor requires a gradient, and the paged operators have none: call them under torch.no_grad()");
+}
+
 struct Scales {
   const float *k, *v;
 };
@@ -153,6 +161,7 @@ Scales scales_of(PyObject* k, PyObject* v, int cache, int H, int dev) {
     return {nullptr, nullptr};
   }
   if (k == Py_None || v == Py_None) refuse("float8_e4m3fn pages need k_scale and v_scale");
+  no_gradient({&tensor(k, "k_scale"), &tensor(v, "v_scale")});
   return {vector<float>(tensor(k, "k_scale"), "k_scale", H, at::kFloat, dev), vector<float>(tensor(v, "v_scale"), "v_scale", H, at::kFloat, dev)};
 }
 
@@ -299,6 +308,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     need_args(n, 9);
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kp = tensor(a[3], "k_pages"), &vp = tensor(a[4], "v_pages");
+    no_gradient({&k, &v, &kp, &vp});
     const int dev = device_of(k, "k");
     const Pool pool = pool_of(kp, vp, dev);
     const int64_t N = k.dim() ? k.size(0) : -1;
@@ -351,6 +361,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     need_args(n, 19);
     const at::Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages");
+    no_gradient({&q, &kp, &vp});
     const int dev = device_of(q, "q");
     const Pool pool = pool_of(kp, vp, dev);
     if (q.dim() != 3 || q.size(2) != pool.E || q.stride(2) != 1 || pool.H == 0 || q.size(1) == 0 || q.size(1) % pool.H)
@@ -414,6 +425,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (padded) out.zero_();
     } else {
       out = tensor(a[15], "out");
+      no_gradient({&out});
       if (!out.sizes().equals({N, Hq, D}) || out.scalar_type() != q.scalar_type() || !on(out, dev) || out.stride(2) != 1)
         refuse("out: expected (" + std::to_string(N) + ", " + std::to_string(Hq) + ", " + std::to_string(D) +
                ") of q's type with a contiguous last axis on cuda:" + std::to_string(dev) + ", got " + place(out));
@@ -423,6 +435,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (a[16] != Py_None) {
       lse = tensor(a[16], "lse");
+      no_gradient({&lse});
       if (!lse.sizes().equals({N, Hq}) || lse.scalar_type() != at::kFloat || !on(lse, dev) || !lse.is_contiguous())
         refuse("lse: expected contiguous float32 (" + std::to_string(N) + ", " + std::to_string(Hq) + ") on cuda:" + std::to_string(dev) + ", got " + place(lse));
     } else if (flag(a[17])) {
