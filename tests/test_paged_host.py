@@ -19,3 +19,38 @@ def test_inputs_that_require_a_gradient_are_refused():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # then the next refusal
             call()
+
+
+def test_the_library_is_built_first_and_without_the_binding(monkeypatch, tmp_path):
+    """Neither g++, nor torch's headers are needed for libthin_attn.so, and a binding that fails to build does not keep it back."""
+    from thinned_softmax_attention_b200 import build as B
+    done = []
+
+    def no_binding():
+        done.append("binding")
+        raise OSError("no compiler")
+
+    monkeypatch.setattr(B, "build_library", lambda verbose=False: done.append("library"))
+    monkeypatch.setattr(B, "build_binding", no_binding)
+    for force, current in ((True, True), (False, False)):
+        monkeypatch.setattr(B, "newer", lambda target, inputs: current)
+        del done[:]
+        with pytest.raises(OSError):
+            B.build(force=force)
+        assert done == ["library", "binding"]
+
+
+def test_the_binding_is_built_anew_for_another_torch(monkeypatch, tmp_path):
+    from thinned_softmax_attention_b200 import build as B
+    stamp = tmp_path / "torch"
+    monkeypatch.setattr(B, "BINDING_TORCH", str(stamp))
+    monkeypatch.setattr(B, "newer", lambda target, inputs: True)
+    assert not B.binding_up_to_date()
+    stamp.write_text(B.torch_version())
+    assert B.binding_up_to_date() and B.up_to_date()
+    monkeypatch.setattr(B, "torch_version", lambda: "0.0")
+    assert not B.binding_up_to_date()
+    built = []
+    monkeypatch.setattr(B, "build_binding", lambda: built.append(1))
+    B.build()
+    assert built == [1]

@@ -13,6 +13,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libthin_attn.so")
 BINDING = os.path.join(HERE, "_paged.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "paged_binding.cpp")
+BINDING_TORCH = os.path.join(ROOT, "_build", "paged_binding.torch")   # the torch that the binding was built against
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
 
@@ -31,8 +32,25 @@ def newer(target, inputs):
     return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in inputs + [__file__])
 
 
+def library_up_to_date():
+    return newer(LIB, sources() + headers())
+
+
+def torch_version():
+    from importlib.metadata import version
+    return version("torch")
+
+
+def binding_up_to_date():
+    try:
+        built_against = open(BINDING_TORCH).read()
+    except OSError:
+        return False
+    return built_against == torch_version() and newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "thin_attn.h")])
+
+
 def up_to_date():
-    return newer(LIB, sources() + headers()) and newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "thin_attn.h")])
+    return library_up_to_date() and binding_up_to_date()
 
 
 def build_binding():
@@ -53,15 +71,21 @@ def build_binding():
                            BINDING_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
                            "-ltorch", "-ltorch_python"])
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_TORCH), exist_ok=True)
+    with open(BINDING_TORCH, "w") as f:
+        f.write(torch_version())
 
 
 def build(force=False, verbose=False):
-    if not force and up_to_date():
-        return LIB
-    if force or not newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "thin_attn.h")]):
+    # the library needs nvcc alone: it is built first, whatever the binding lacks
+    if force or not library_up_to_date():
+        build_library(verbose)
+    if force or not binding_up_to_date():
         build_binding()
-    if not force and newer(LIB, sources() + headers()):
-        return LIB
+    return LIB
+
+
+def build_library(verbose=False):
     nvcc = os.environ.get("NVCC", "nvcc")
     objdir = os.path.join(ROOT, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -88,7 +112,6 @@ def build(force=False, verbose=False):
     subprocess.check_call([nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs,
                            "-Xcompiler", "-fPIC", "-cudart", "static"])
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
