@@ -395,7 +395,7 @@ THIN_ATTN_API thin_attn_status thin_attn_paged_release(const thin_attn_paged_rel
 
 /* Write keys and values of N tokens into their slots; a token whose slot lies outside the pool
  * (-1 for padding) is skipped.  cache_dtype: dtype, or E4M3 with dtype BF16 or FP16: the cache then
- * holds x / scale[h] rounded to the nearest e4m3 value, at most 448 in magnitude.
+ * holds x / scale[h], as fp32 has it, rounded to the nearest e4m3 value, at most 448 in magnitude.
  * With bounds: int8 (n_pages, H, 2, E) and exps int8 (n_pages, H) are brought up to date.  For the keys
  * k that the cache holds of a page and head (a NaN counts as 0), m = max |k|: the exponent x is the least integer
  * in [-40, 48] with 127 * 2^x >= m (48 if none), bounds row 0 = floor(min k / 2^x), row 1 =

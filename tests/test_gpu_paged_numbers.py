@@ -161,3 +161,28 @@ def test_a_gradient_is_not_dropped_in_silence():
             call()
         with torch.no_grad():
             call()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_quotients_next_to_the_borders_of_e4m3(dtype):
+    """x / scale on and one step either side of every border between two e4m3 values, at every mantissa of x, up to where
+    it is clamped: the bytes of the rounded quotient."""
+    bits = 10 if dtype == "fp16" else 7
+    border = [(k + 0.5) * 2.0 ** -9 for k in range(8)] + [(1 + (k + 0.5) / 8) * 2.0 ** e for e in range(-6, 9) for k in range(8)]
+    E, page = 64, 1 << bits
+    x = (1 + torch.arange(1 << bits, device=DEV) / (1 << bits)).to(TYPES[dtype])
+    m = torch.tensor(border, device=DEV)
+    near = (x.float()[:, None] / m).view(-1)                                  # scales that lead to the border
+    steps = torch.arange(-2, 3, device=DEV, dtype=torch.int32)
+    scales = (near.view(torch.int32)[:, None] + steps).view(torch.float32)    # (mantissas x borders, 5)
+    n = 4096                                                                  # heads of a call: a scale each
+    xs = x[:, None].expand(-1, m.numel()).reshape(-1)
+    for u in range(5):
+        for i in range(0, xs.numel(), n):
+            s, y = scales[i:i + n, u].contiguous(), xs[i:i + n]
+            H = s.numel()
+            k = torch.stack([y, -y], -1).repeat(1, 8)[None].contiguous()      # (1, H, 16)
+            kp, vp = (torch.zeros(1, H, 1, 16, device=DEV).to(TYPES["e4m3"]) for _ in range(2))
+            T.paged_append(k, k, torch.zeros(1, dtype=torch.int64, device=DEV), kp, vp, k_scale=s, v_scale=s)
+            want = (k[0].float() / s[:, None]).clamp(-448, 448).to(TYPES["e4m3"])
+            assert torch.equal(kp[0, :, 0].float(), want.float()) and torch.equal(vp[0, :, 0].float(), want.float())

@@ -30,10 +30,12 @@ constexpr int kPieces = 4;            // pieces of keys that a thread copies
 constexpr int kShort = 16;            // tokens of a run that one warp takes
 
 // x / scale by the rounded reciprocal and one correction of the remainder (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990): the rounded quotient, one step of
-// fp32 off in about 1 of 10^8 pairs, which the rounding to 4 bits behind it does not see.  It has no branch, so
-// the rows' loads stay together.  Very large quotients go uncorrected (they are clamped), scales of unusual size
-// by division.
+// elementary functions on the IBM RISC System/6000 processor", 1990): what is wrong with the reciprocal enters the
+// remainder's share alone, so the result differs from the rounded quotient only where x / scale lies within 2^-23 of a
+// step of the middle between two fp32 numbers.  Next to a border of two e4m3 values, where alone the byte would tell, there is no such x
+// of 8 or 11 bits: all their mantissas, with the scales up to three steps around x / border, give the rounded quotient.
+// It has no branch, so the rows' loads stay together.  Very large quotients go uncorrected (they are clamped), scales of
+// unusual size by division.
 struct Quotient {
   float scale, inverse;
   bool plain;
