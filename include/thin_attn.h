@@ -335,7 +335,7 @@ THIN_ATTN_API thin_attn_status thin_attn_halve_noalloc(int dtype, const void* K,
  *
  *   k_pages (n_pages, H, page, E), v_pages (n_pages, H, page, D)   any strides, last axis contiguous
  *   table   (R, W) int32      page ids of request r in token order, rows table_row ids apart
- *   slot    page id * page + offset: the place of one token in the pool
+ *   slot    page id * page + offset: the place of one token in the pool, page at most 65536
  *
  * These entry points take one argument struct each (struct_size = its sizeof), run on its device, on
  * the caller's stream, and keep no state: no handle, no allocation, scratch only where the caller
@@ -347,7 +347,7 @@ THIN_ATTN_API thin_attn_status thin_attn_halve_noalloc(int dtype, const void* K,
 
 /* Slots, block tables and the free stack of a step that gives request r n_new[r] more tokens.
  * Requests are served in order.  status[r]:
- *   0  placed (n_new = 0 included)
+ *   0  placed (one with n_new = 0 too, unless 2 or 3 is true of it)
  *   1  the free stack is short of pages for it, or was for an earlier request and it needs one too
  *   2  its row of the table is too narrow, or lengths[r] or n_new[r] is negative
  *   3  its tokens end behind max_tokens

@@ -8,9 +8,12 @@
 // behind the block), and a warp per run joins them.  The exponent x is monotone in max |k|, and
 // floor(floor(u) / 2^s) = floor(u / 2^s), so widening stored bounds step by step gives the bounds
 // that all of the page's keys together would.
-// Each row is read and written once.  B200, 16384 tokens of 8 heads of width 128: 25 us in bf16 without
-// bounds (134 MB, 85% of the copy rate), 37 with them, 43 into e4m3 (27 without); there instructions bound it (a page
-// of 64 keys is some 1200 of them per warp of its CTA).  64 tokens, one page each: 2.6 us without, 6.4 with.
+// Each row is written once.  For the bounds the keys of short runs, and those of a run behind its block, are read and
+// rounded again, from L1 and L2 (DRAM: 68 MB read of 67): about half of all keys with pages of 64 that begin anywhere.  One
+// CTA per head takes the whole of a run, so that pages much longer than a block are slow where bounds are kept.
+// B200, 16384 tokens of 8 heads of width 128: 25 us in bf16 without bounds (134 MB, 85% of the copy rate), 37 with them, 43
+// into e4m3 (27 without); there instructions bound it (issue slots 56% and 67% busy with 43% of the warps; a page of 64
+// keys is some 1200 of them per warp of its CTA).  64 tokens, one page each: 2.6 us without, 6.5 with.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -35,15 +35,16 @@
 //
 // These are the 16-row products on purpose: tcgen05 tiles have 64 or 128 rows, of which G would fill a few,
 // and their operands pass through shared memory in fixed layouts, P included.  The tensor pipe is no bound here
-// (24% busy at e4m3, the densest case).
+// (32% busy at e4m3, the densest case of up to 8 rows; issue slots 52%).
 //
 // B200 (copy rate 6.46 TB/s), width 128, bf16, 4 query rows to a key head unless stated:
-//   16 requests of 65536 .. 131072 keys, 8 heads     0.91 .. 0.95 ms   6.9 .. 6.6 TB/s
-//   48 requests of 1 .. 8192 keys, 8 heads           54 us             5.5 TB/s     16 query rows: 63 us
-//   20 requests of 32768 keys, 8 heads, e4m3         0.22 ms           6.0 TB/s
-//   16 requests of up to 65536 keys, fp32            1.7 ms            5.0 TB/s
+//   16 requests of 65536 .. 131072 keys, 8 heads     0.89 .. 0.95 ms   7.0 .. 6.6 TB/s
+//   48 requests of 1 .. 8192 keys, 8 heads           54 us             5.5 TB/s     16 query rows: 64 us
+//   40 requests of 32768 keys, 4 heads, e4m3         0.23 ms           5.8 TB/s     16 query rows: 0.25, fp16 0.32 ms
+//   16 requests of 32768 .. 65536 keys, fp32         1.32 ms           4.8 TB/s     width 256, 48 of 8192: 3.5 TB/s
 //   1 request of 500 keys, 32 heads                  9.8 us            (6.4 of them with 64 keys)
-// What is left is the 10 us at the ends: launch, lengths, first reads, join.
+// What is left of the first three is the 10 us at the ends: launch, lengths, first reads, join.  In fp32 it is the splitting
+// of every key and value into its two parts, and at width 256 one CTA per SM with two short stages.
 #include <type_traits>
 
 #include "paged.h"
@@ -1044,7 +1045,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(PagedAttn p, Part
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Query rows of a tile: up to 8 leave its upper half for the operands' lower parts, 9 to 16 fill it (fp32 has
-// only the first form); more are several tiles, whose keys come from L2 for all but one.
+// only the first form); more are several tiles, each a pair of its own on the line that reads the keys again (the 48
+// requests above with 16 rows 64 us, with 32 113; as many draft tokens of a request are as many pairs too: four 176).
 int rows_of(const thin_attn_paged_attention_args& a) {
   return a.dtype == THIN_ATTN_FP32 || a.Hq / a.H <= 8 ? 8 : 16;
 }
@@ -1097,7 +1099,7 @@ cudaError_t launch_tile(const PagedAttn& p, void* ws, cudaStream_t st) {
 
 // By the wider of E and D, rounded up to the stage's row; narrower rows are padded in shared memory, not in
 // the reads.  Warps, stages and CTAs per SM fill the 227 KB with 64 KB and more of reads in flight per SM.  Rows of up to
-// 128 bytes come 32 keys to a stage (16 keys: the e4m3 requests above 0.26 ms).
+// 128 bytes come 32 keys to a stage (the e4m3 requests above in stages of 16 keys: a sixth more time).
 template <typename T, int ROWS>
 cudaError_t launch_mma(const PagedAttn& p, void* ws, cudaStream_t st) {
   const int w = p.a.E > p.a.D ? p.a.E : p.a.D;

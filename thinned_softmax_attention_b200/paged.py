@@ -48,7 +48,8 @@ class PagedPlan(NamedTuple):
     """A step's places.  ``lengths`` (R) and ``n_free`` (1) after the step; ``cu`` (R + 1) the prefix
     sums of the new lengths; per token of the step ``slots`` int64, ``rows`` (its request) and
     ``context`` (the keys it sees, itself among them), -1, -1 and 0 where there is none; ``status``
-    (R): 0 placed, 1 out of pages, 2 table row too narrow or a negative length, 3 behind max_tokens."""
+    (R): 0 placed, 1 out of pages, 2 table row too narrow or a negative length, 3 behind max_tokens (a
+    request without new tokens too, where those before it fill the step)."""
     lengths: torch.Tensor
     n_free: torch.Tensor
     cu: torch.Tensor
@@ -87,7 +88,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
                  bounds: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> None:
     """Write k (N, H, E) and v (N, H, D) into their slots; a slot outside the pool (-1) is skipped.
 
-    float8_e4m3fn pages hold x / scale[h], rounded to the nearest value, at most 448 in magnitude.
+    float8_e4m3fn pages hold x / scale[h], rounded to the nearest value, at most 448 in magnitude.  k and
+    v may not be rows that the call writes.
     ``bounds`` = (int8 (n_pages, H, 2, E), int8 (n_pages, H)): the pages' key bounds for
     ``paged_sparse_attention``, widened by the new keys, or started anew where a page's first slot
     is written; the tokens of one page must then be neighbours, as ``paged_plan`` lays them, with no skipped
