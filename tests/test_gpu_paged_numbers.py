@@ -186,3 +186,16 @@ def test_quotients_next_to_the_borders_of_e4m3(dtype):
             T.paged_append(k, k, torch.zeros(1, dtype=torch.int64, device=DEV), kp, vp, k_scale=s, v_scale=s)
             want = (k[0].float() / s[:, None]).clamp(-448, 448).to(TYPES["e4m3"])
             assert torch.equal(kp[0, :, 0].float(), want.float()) and torch.equal(vp[0, :, 0].float(), want.float())
+
+
+@pytest.mark.parametrize("G", [1, 8, 20])
+def test_weights_in_fp32_keep_21_bits(G):
+    """Two keys of nearly equal weight and opposite values.  The larger weight is 1; the other is off by the exponential's
+    2^-22 and the 2^-22 that it is cut by, half of which reaches the output, whose sum of weights is rounded by 2^-24."""
+    E, page = 64, 16
+    kp, vp = (torch.zeros(1, 1, page, E, device=DEV) for _ in range(2))
+    kp[0, 0, 0, 0], kp[0, 0, 1, 0], vp[0, 0, 0], vp[0, 0, 1] = 1.0, -1.0, 1.0, -1.0
+    q = torch.zeros(8, G, E, device=DEV)
+    q[..., 0] = (torch.arange(1, 8 * G + 1, device=DEV) * 1.37e-4).view(8, G)
+    out = T.paged_attention(q, kp, vp, i32([[0]] * 8), i32([2] * 8), scale=1.0)
+    assert ((out.double() - torch.tanh(q[..., :1].double())).abs() <= 2.0 ** -21).all()
