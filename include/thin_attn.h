@@ -449,7 +449,7 @@ THIN_ATTN_API thin_attn_status thin_attn_paged_append(const thin_attn_paged_appe
 typedef struct {
   uint32_t struct_size;
   int32_t device, dtype, cache_dtype, N, R, W, Hq, H, E, D, page, n_pages, window, top, first, last;
-  float scale;               /* 0 selects 1/sqrt(E); negative: refused */
+  float scale;               /* 0 selects 1/sqrt(E); negative, above 2.3e38: refused */
   const void* q;             /* (N, Hq, E), strides in elements */
   int64_t q_token, q_head;
   const void* k_pages;

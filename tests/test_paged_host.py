@@ -54,3 +54,10 @@ def test_the_binding_is_built_anew_for_another_torch(monkeypatch, tmp_path):
     monkeypatch.setattr(B, "build_binding", lambda: built.append(1))
     B.build()
     assert built == [1]
+
+
+def test_scales_beyond_fp32_are_refused():
+    """scale log2 e, which the kernel multiplies scores by, would be infinite, and a score of 0 NaN."""
+    from tests.test_paged import refused
+    for scale in (2.4e38, 3.4e38, float("inf"), float("nan"), -1e-30):
+        refused("attention", scale=scale)

@@ -62,7 +62,8 @@ thin_attn_status check_attention(const thin_attn_paged_attention_args* a) {
   if ((int64_t)a->N * a->Hq > kIntMax / 64) return err(THIN_ATTN_EINVAL, "N * Hq = %lld too large", (long long)a->N * a->Hq);
   if ((int64_t)a->W * a->page > kIntMax - 4096) return err(THIN_ATTN_EINVAL, "W * page = %lld too large", (long long)a->W * a->page);
   if (!a->rows && a->N > a->R) return err(THIN_ATTN_EINVAL, "%d tokens without rows over %d requests", a->N, a->R);
-  if (!(a->scale >= 0.f) || std::isinf(a->scale)) return err(THIN_ATTN_EINVAL, "scale=%g", a->scale);
+  if (!(a->scale >= 0.f && a->scale <= 2.3e38f))   // scale log2 e is a finite number too
+    return err(THIN_ATTN_EINVAL, "scale=%g: expected 0 to 2.3e38", a->scale);
   if (a->window < 0) return err(THIN_ATTN_EINVAL, "window=%d", a->window);
   if (a->top < 0 || a->top > kMaxTop) return err(THIN_ATTN_EINVAL, "top=%d outside 0..%d", a->top, kMaxTop);
   if (a->top) {

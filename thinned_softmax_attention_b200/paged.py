@@ -113,7 +113,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     are several rows of q with lengths that grow by one (``paged_plan``'s ``rows`` and ``context``).  One that sees
     nothing gets zeros and -inf; one whose row is negative is padding and leaves its rows of
     ``out`` and ``lse`` as they were (zeros in buffers made here).
-    ``scale`` (without it 1 / sqrt(E)) is positive and finite.
+    ``scale`` (without it 1 / sqrt(E)) is positive and at most 2.3e38.
     The keys are read once per query token: made for decode and short drafts, not for long prompts."""
     got = _calls().attention(q, k_pages, v_pages, table, lengths, rows, scale, k_scale, v_scale, window, None, None, 0, 0, 0, out, lse,
                              return_lse, False)
