@@ -54,7 +54,7 @@ def test_very_long_sums_of_16_bit_types_do_not_drift(dtype, cache, width, G, key
 @pytest.mark.parametrize("G", [4, 8, 12, 16])
 def test_weights_against_an_8_bit_cache_keep_more_than_16_bits(G):
     """Two keys of nearly equal weight and opposite values: what a weight loses is the output's error.  A weight in one
-    fp16 number would be off by up to 2^-12, the tolerance takes it as good to 2^-16 (its two parts: 2^-22)."""
+    fp16 number would be off by up to 2^-11, the tolerance takes it as good to 2^-16 (its two parts: 2^-22)."""
     E, page = 64, 16
     kp, vp = (torch.zeros(1, 1, page, E, device=DEV) for _ in range(2))
     kp[0, 0, 0, 0], kp[0, 0, 1, 0], vp[0, 0, 0], vp[0, 0, 1] = 1.0, -1.0, 1.0, -1.0

@@ -23,7 +23,7 @@
 // lane (r, c) holds the columns of keys 4 c .. 4 c + 3, reads those four rows of V as 16-byte pieces
 // (of d = DC (r + 8 i) ..) and pairs them up with byte permutations.  No transposing load, no shuffle but
 // the row maximum.  G <= 8 leaves the tile's upper 8 rows free: they carry P's rounding error, so P
-// keeps 16 bits and more at no cost; G <= 16 issues that product separately.
+// keeps 16 bits and more at no cost; G <= 16 issues that product separately (bf16 against e4m3: none, kSplit).
 //
 // fp32 caches use the tf32 products (m16n8k8) with every operand as the sum of two tf32 numbers,
 // (a_hi + a_lo)(b_hi + b_lo), good to 2^-22.  The upper rows of the tile carry a_lo, so that takes two products.
@@ -171,7 +171,7 @@ struct MmaTile {
   static constexpr int DC = 16 / (int)sizeof(C);              // elements of a 16-byte piece
   static constexpr int KJ = RB / 64, VI = RB / 128;           // pieces of K and V per lane and row
   static constexpr int QW = DC / 2;                           // words of Q per piece
-  // P as two numbers.  One is enough for 16 bf16 rows against e4m3: off by 2^-12 at most, an eighth of what the output is
+  // P as two numbers.  One is enough for 16 bf16 rows against e4m3: off by 2^-11 at most, an eighth of what the output is
   // rounded by; the second product would take 252 us to 299 (40 requests of 32768 keys; fp16 282 to 320)
   static constexpr bool kSplit = !k8 || ROWS == 8 || std::is_same<T, __half>::value;
   static constexpr int kKeys = RB <= 128 ? 32 : 16;           // keys of a stage: short rows, twice as many for the same overhead
@@ -180,8 +180,8 @@ struct MmaTile {
   // tail of keys at 2^-25 is rounded up or away as a whole
   static constexpr float kLift = std::is_same<M, __half>::value ? 16384.f : 1.f;
   // With 16 rows one sum takes both parts' products, and an infinite value must meet two parts of one sign: the leading
-  // one is cut, and the lower one is made no less than the least step.  (Leaving infinities out of the lower product
-  // instead took 5% to 10%; e4m3 has none.)
+  // one is cut, and the lower one is made positive, in bf16 by the weight's last bit, in fp16 by the least step.  (Leaving
+  // infinities out of the lower product instead took 5% to 10%; e4m3 has none.)
   static constexpr bool kOneSign = ROWS == 16 && !k8;
   static_assert(ROWS == 8 || ROWS == 16, "");
   static_assert(VI >= 1 && KJ == 2 * VI, "");
